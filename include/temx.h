@@ -12,7 +12,10 @@
  *     quantization and the GEMM, with the scales cast to E8M0 or as FP32;
  *   - the MXFP8 x MXFP8 -> fp32-accumulate GEMM with bias, GELU(tanh) and
  *     GELU-aux (pre-activation) epilogues;
- *   - a single-launch grouped (MoE) variant over ragged expert row counts.
+ *   - a single-launch grouped (MoE) variant over ragged expert row counts;
+ *   - layer norm / RMS norm, forward and backward, and the gated
+ *     feed-forward GEMMs (both projections, activation and product in one
+ *     kernel), forward and backward, dense and grouped.
  *
  * Sources, cited by page title and section:
  *   [ROCm-TE]  "Transformer Engine On ROCm and AMDGPU" (ROCm/TransformerEngine
@@ -101,6 +104,11 @@ typedef enum {
   TE_BLOCK_SCALES_E8M0 = 0, /* cast to E8M0 (smallest power of two >= s) first: the gfx950 default */
   TE_BLOCK_SCALES_FP32 = 1  /* the FP32 scales themselves */
 } te_block_scaling;
+
+typedef enum { TE_NORM_LAYER = 0, TE_NORM_RMS = 1 } te_norm_kind;
+
+/* The gate activation of a gated feed-forward block (TE_ACT_GELU: the tanh form). */
+typedef enum { TE_ACT_SILU = 0, TE_ACT_GELU = 1 } te_activation;
 
 /* Human-readable name of a status code (static storage). */
 const char* te_status_str(te_status status);
@@ -419,6 +427,134 @@ te_status te_fp8_block_gemm(const uint8_t* a, const float* a_scale_inv, te_dtype
                             void* d, te_dtype d_dtype, te_epilogue epi,
                             const uint16_t* bias, uint16_t* aux, te_block_scaling mode, float beta,
                             void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Layer norm / RMS norm of the rows of x, with an optional residual add in
+ * front and an optional MXFP8 output: what precedes the first GEMM of a
+ * LayerNormLinear / LayerNormMLP block.
+ *   s    = x + residual, rounded to dtype (s = x without a residual)
+ *   mean = sum_c s / cols (0 for TE_NORM_RMS)
+ *   rstd = 1 / sqrt(sum_c (s - mean)^2 / cols + eps)
+ *   y    = (s - mean) * rstd * gamma + beta
+ * Statistics and arithmetic are fp32; y is rounded once.
+ *   x, residual, sum_out, y   dtype [rows, cols]: TE_BF16, TE_FP16 or TE_FP32
+ *   residual, sum_out   both or neither; sum_out (s, what the backward takes
+ *                as x) may be x or residual itself
+ *   gamma, beta  w_dtype [cols], w_dtype = dtype or TE_FP32; beta may be NULL
+ *                (no bias) and must be with TE_NORM_RMS
+ *   eps          >= 0, finite
+ *   y            may be NULL where q is given
+ *   q, q_scale   both or neither: the rowwise MXFP8 operand (q_fmt TE_E4M3 or
+ *                TE_E5M2) of the bf16 y, exactly as te_mxfp8_quantize
+ *                (TE_ROWWISE) gives it; needs dtype TE_BF16 and
+ *                cols % 32 == 0.  q_fmt is ignored without them.
+ *   mean, rstd   float [rows]: the statistics the backward takes, or NULL
+ *                (both, with TE_NORM_LAYER; mean is NULL with TE_NORM_RMS)
+ *   rows, cols   any number >= 0 (below 2^31 - 65536); an empty tensor
+ *                enqueues nothing.  No other output may overlap an input.
+ *   All tensors are 16-byte aligned (TE_ERR_ALIGN); a non-finite value
+ *   affects its own row only.
+ */
+te_status te_norm_forward(te_norm_kind kind, const void* x, te_dtype dtype, int64_t rows, int64_t cols,
+                          const void* residual, const void* gamma, const void* beta, te_dtype w_dtype, float eps,
+                          void* sum_out, void* y, uint8_t* q, uint8_t* q_scale, te_dtype q_fmt, float* mean,
+                          float* rstd, hipStream_t stream);
+
+/*
+ * The backward pass of te_norm_forward.  With xh = (x - mean) rstd and
+ * g = dy gamma:
+ *   dx     = rstd (g - sum_c g / cols - xh sum_c (g xh) / cols) + dskip
+ *            (TE_NORM_RMS: without the sum_c g term, and mean = 0)
+ *   dgamma = sum_r dy xh,   dbeta = sum_r dy
+ * Arithmetic and sums are fp32 in a fixed order (deterministic); each output
+ * is rounded once.
+ *   dy, x, dskip, dx   dtype [rows, cols]; x is the normalised tensor (the
+ *                forward's sum_out where it had a residual); dskip, the
+ *                gradient that reaches x by the skip path, may be NULL
+ *   gamma, dgamma, dbeta   w_dtype [cols]; dbeta may be NULL (not wanted) and
+ *                must be with TE_NORM_RMS
+ *   mean, rstd   float [rows] as the forward gave them (mean NULL with
+ *                TE_NORM_RMS)
+ *   workspace    device scratch of at least
+ *                te_norm_backward_workspace_size(rows, cols) bytes, 16-byte
+ *                aligned: fp32 partial sums of the weight gradients.  Calls
+ *                that may run at the same time need workspaces of their own.
+ *   dx may be dskip itself; no other output may overlap an input.
+ *   rows == 0 writes zeros to dgamma and dbeta; cols == 0 enqueues nothing.
+ */
+size_t te_norm_backward_workspace_size(int64_t rows, int64_t cols);
+te_status te_norm_backward(te_norm_kind kind, const void* dy, const void* x, const void* dskip, te_dtype dtype,
+                           int64_t rows, int64_t cols, const void* gamma, te_dtype w_dtype, const float* mean,
+                           const float* rstd, void* dx, void* dgamma, void* dbeta, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gated feed-forward GEMM, "TN", MXFP8 operands as te_mxfp8_gemm: both
+ * projections, the activation and the product in one kernel.
+ *   P = A . B^T + bias  [M, 2N]: columns 0 .. N-1 the gate, N .. 2N-1 the up
+ *                       projection;
+ *   D[m, n] = act(P[m, n]) * P[m, N + n],   fp32 up to one rounding of D.
+ *   a        uint8 [M, K] + a_scale [M, K/32]; b uint8 [2N, K] + b_scale
+ *            [2N, K/32], the N gate rows first; E5M2 x E5M2 is rejected
+ *   act      TE_ACT_SILU or TE_ACT_GELU (tanh form)
+ *   d        TE_BF16: bf16 [M, N], d_scale NULL.  TE_E4M3 / TE_E5M2: uint8
+ *            [M, N] codes with E8M0 scales d_scale [M, N/32], bit-identical
+ *            to te_mxfp8_quantize (TE_ROWWISE) of the bf16 D; N % 32 == 0
+ *   bias     bf16 [2N], or NULL
+ *   aux      bf16 [M, 2N] = P, what the backward needs, or NULL
+ *   Shapes: K % 128 == 0, N % 16 == 0, any M >= 0 (single tokens too);
+ *   K <= 2^23, 2N and M < 2^31 - 256, 2N K / 32 < 2^31 - 4096.
+ *   M == 0 or N == 0 enqueues nothing; K == 0 gives P = bias.
+ *   workspace: optional, as te_mxfp8_gemm's (te_mxfp8_gated_gemm_workspace_size
+ *   bytes enable the faster path; same results without).
+ */
+size_t te_mxfp8_gated_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
+te_status te_mxfp8_gated_gemm(const uint8_t* a, const uint8_t* a_scale, te_dtype a_fmt, const uint8_t* b,
+                              const uint8_t* b_scale, te_dtype b_fmt, int64_t M, int64_t N, int64_t K,
+                              te_activation act, void* d, uint8_t* d_scale, te_dtype d_dtype, const uint16_t* bias,
+                              uint16_t* aux, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Backward of the gated feed-forward GEMM: the gradients of both
+ * pre-activations from the output gradient's GEMM through the next (down)
+ * projection, in its epilogue.
+ *   acc = A . B^T  [M, N]  (A = dY, B = the transposed copy of the down
+ *                           projection's weights)
+ *   D[m, n]     = acc * up * act'(gate),
+ *   D[m, N + n] = acc * act(gate),   gate = aux[m, n], up = aux[m, N + n]
+ *   a        uint8 [M, K] + a_scale; b uint8 [N, K] + b_scale
+ *   aux      bf16 [M, 2N]: the forward's saved pre-activations
+ *   d        bf16 [M, 2N]
+ *   Shapes, workspace: as te_mxfp8_gated_gemm.  aux and d must not overlap.
+ */
+size_t te_mxfp8_dgated_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
+te_status te_mxfp8_dgated_gemm(const uint8_t* a, const uint8_t* a_scale, te_dtype a_fmt, const uint8_t* b,
+                               const uint8_t* b_scale, te_dtype b_fmt, int64_t M, int64_t N, int64_t K,
+                               te_activation act, const uint16_t* aux, uint16_t* d, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The two GEMMs above over ragged groups of rows (experts) in one launch:
+ * group g owns rows [off_g, off_g + m_splits[g]) of A, D and aux and its own
+ * B (and bias) as in te_mxfp8_grouped_gemm.
+ *   num_groups  1 .. 1024
+ *   m_splits    int32 [G], DEVICE memory.  Precondition: every split >= 0,
+ *               their sum <= total_m; rows behind the last group stay as they
+ *               were.  Bad splits cannot read or write outside the tensors,
+ *               but their results are unspecified.
+ *   b           uint8 [G * 2N, K] (forward: each group's gate rows, then its
+ *               up rows) or [G * N, K] (backward); b_scale likewise
+ *   bias        bf16 [G, 2N], or NULL
+ *   Shapes as above, and N, K > 0.
+ */
+te_status te_mxfp8_grouped_gated_gemm(int32_t num_groups, const int32_t* m_splits, int64_t total_m, const uint8_t* a,
+                                      const uint8_t* a_scale, te_dtype a_fmt, const uint8_t* b,
+                                      const uint8_t* b_scale, te_dtype b_fmt, int64_t N, int64_t K, te_activation act,
+                                      uint16_t* d, const uint16_t* bias, uint16_t* aux, hipStream_t stream);
+te_status te_mxfp8_grouped_dgated_gemm(int32_t num_groups, const int32_t* m_splits, int64_t total_m, const uint8_t* a,
+                                       const uint8_t* a_scale, te_dtype a_fmt, const uint8_t* b,
+                                       const uint8_t* b_scale, te_dtype b_fmt, int64_t N, int64_t K,
+                                       te_activation act, const uint16_t* aux, uint16_t* d, hipStream_t stream);
 
 #ifdef __cplusplus
 }

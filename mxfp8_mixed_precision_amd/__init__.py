@@ -28,6 +28,10 @@ TE_ROWWISE, TE_COLWISE, TE_BOTH = 1, 2, 3
 TE_AMAX_MAX, TE_AMAX_MOST_RECENT = 0, 1
 AMAX_ALGOS = {"max": TE_AMAX_MAX, "most_recent": TE_AMAX_MOST_RECENT}
 TE_BLOCK_SCALES_E8M0, TE_BLOCK_SCALES_FP32 = 0, 1
+TE_NORM_LAYER, TE_NORM_RMS = 0, 1
+NORM_KINDS = {"layer": TE_NORM_LAYER, "rms": TE_NORM_RMS}
+TE_ACT_SILU, TE_ACT_GELU = 0, 1
+ACTIVATIONS = {"silu": TE_ACT_SILU, "gelu": TE_ACT_GELU}
 BLOCK_SCALINGS = {"e8m0": TE_BLOCK_SCALES_E8M0, "fp32": TE_BLOCK_SCALES_FP32}
 
 FORMATS = {"e4m3": TE_E4M3, "e5m2": TE_E5M2}
@@ -63,6 +67,21 @@ _SIGS = {
     "te_fp8_block_gemm": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _vp, _vp, ctypes.c_int, ctypes.c_int, _i64, _i64,
                                          _i64, _vp, ctypes.c_int, ctypes.c_int, _vp, _vp, ctypes.c_int, ctypes.c_float,
                                          _vp, _sz, _vp]),
+    "te_norm_forward": (ctypes.c_int, [ctypes.c_int, _vp, ctypes.c_int, _i64, _i64, _vp, _vp, _vp, ctypes.c_int,
+                                       ctypes.c_float, _vp, _vp, _vp, _vp, ctypes.c_int, _vp, _vp, _vp]),
+    "te_norm_backward_workspace_size": (_sz, [_i64, _i64]),
+    "te_norm_backward": (ctypes.c_int, [ctypes.c_int, _vp, _vp, _vp, ctypes.c_int, _i64, _i64, _vp, ctypes.c_int,
+                                        _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "te_mxfp8_gated_gemm_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "te_mxfp8_gated_gemm": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _vp, _vp, ctypes.c_int, _i64, _i64, _i64,
+                                           ctypes.c_int, _vp, _vp, ctypes.c_int, _vp, _vp, _vp, _sz, _vp]),
+    "te_mxfp8_dgated_gemm_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "te_mxfp8_dgated_gemm": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _vp, _vp, ctypes.c_int, _i64, _i64, _i64,
+                                            ctypes.c_int, _vp, _vp, _vp, _sz, _vp]),
+    "te_mxfp8_grouped_gated_gemm": (ctypes.c_int, [_i32, _vp, _i64, _vp, _vp, ctypes.c_int, _vp, _vp, ctypes.c_int,
+                                                   _i64, _i64, ctypes.c_int, _vp, _vp, _vp, _vp]),
+    "te_mxfp8_grouped_dgated_gemm": (ctypes.c_int, [_i32, _vp, _i64, _vp, _vp, ctypes.c_int, _vp, _vp, ctypes.c_int,
+                                                    _i64, _i64, ctypes.c_int, _vp, _vp, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -383,6 +402,195 @@ def te_fp8_block_gemm(a, a_scale_inv, a_fmt, b, b_scale_inv, b_fmt, b_block_2d, 
         _ptr(a), _ptr(a_scale_inv), _fmt(a_fmt), _ptr(b), _ptr(b_scale_inv), _fmt(b_fmt), int(bool(b_block_2d)),
         M, N, K, _ptr(d), d_dtype, epi, _ptr(bias), _ptr(aux), _block_scaling(mode), float(beta), _ptr(workspace),
         ws_bytes, _stream(stream)))
+
+
+# -------------------------------------------- norms and gated feed-forward GEMMs
+
+_NORM_DTYPES = {torch.bfloat16: TE_BF16, torch.float16: TE_FP16, torch.float32: TE_FP32}
+
+
+class _Call:
+    """One call of the entry points below: its tensors' checks, device and stream.  Every tensor has to be dense,
+    of the stated type and shape, and on the first one's device, which is the device the call runs on whatever the
+    current one is."""
+
+    __slots__ = ("device",)
+
+    def __init__(self, first, name):
+        _require(isinstance(first, torch.Tensor), f"{name} is required")
+        self.device = first.device
+
+    def ptr(self, t, name, shape, dtypes, kind):
+        """Device address of a required tensor."""
+        if t is None:
+            raise ValueError(f"{name} is required")
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name}: expected {kind}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, the first tensor on {self.device}")
+        return _ptr(t)
+
+    def opt(self, t, name, shape, dtypes, kind):
+        """Device address of an optional tensor (None stays None)."""
+        return None if t is None else self.ptr(t, name, shape, dtypes, kind)
+
+    def workspace(self, t):
+        """(address, bytes) of an optional workspace."""
+        if t is None:
+            return None, 0
+        if t.device != self.device:
+            raise ValueError(f"workspace is on {t.device}, the first tensor on {self.device}")
+        return _ptr(t), t.numel() * t.element_size()
+
+    def run(self, name, args, stream):
+        """The call with the tensors' device current, on `stream` or that device's current stream."""
+        if self.device.type != "cuda":
+            raise ValueError(f"expected a GPU tensor, got one on {self.device}")
+        if self.device.index == torch.cuda.current_device():
+            status = getattr(_lib, name)(*args, _stream(stream))
+        else:
+            with torch.cuda.device(self.device):
+                status = getattr(_lib, name)(*args, _stream(stream))
+        if status != TE_OK:
+            raise TemxError(name, status)
+
+
+_FLOAT_KIND = "bfloat16, float16 or float32"
+_U8 = frozenset(_BYTE_DTYPES)
+_B16 = frozenset(_BF16_DTYPES)
+_F32 = frozenset((torch.float32,))
+_I32 = frozenset((torch.int32,))
+
+
+def _norm_args(kind, x, gamma):
+    """(call, kind, rows, cols, x's dtype code and dtypes, gamma's dtype code and dtypes)"""
+    call = _Call(x, "x")
+    k = NORM_KINDS[kind] if isinstance(kind, str) else int(kind)
+    _require(x.dim() == 2, "x must be 2-D")
+    rows, cols = x.shape
+    _require(x.dtype in _NORM_DTYPES, f"x: expected {_FLOAT_KIND}, got {x.dtype}")
+    _require(gamma is not None and (gamma.dtype == x.dtype or gamma.dtype == torch.float32),
+             "gamma: expected x's dtype or float32")
+    return call, k, rows, cols, _NORM_DTYPES[x.dtype], (x.dtype,), _NORM_DTYPES[gamma.dtype], (gamma.dtype,)
+
+
+def te_norm_forward(kind, x, gamma, beta=None, eps=1e-5, y=None, q=None, q_scale=None, q_fmt="e4m3", residual=None,
+                    sum_out=None, mean=None, rstd=None, stream=None) -> None:
+    call, k, rows, cols, dt, xd, wdt, wd = _norm_args(kind, x, gamma)
+    full, w = (rows, cols), (cols,)
+    if q is not None:
+        _require(cols % 32 == 0, "q: the MXFP8 output needs cols % 32 == 0")
+    call.run("te_norm_forward", (
+        k, call.ptr(x, "x", full, xd, xd[0]), dt, rows, cols, call.opt(residual, "residual", full, xd, xd[0]),
+        call.ptr(gamma, "gamma", w, wd, wd[0]), call.opt(beta, "beta", w, wd, wd[0]), wdt, float(eps),
+        call.opt(sum_out, "sum_out", full, xd, xd[0]), call.opt(y, "y", full, xd, xd[0]),
+        call.opt(q, "q", full, _U8, "1-byte codes (uint8)"),
+        call.opt(q_scale, "q_scale", (rows, cols // 32), _U8, "1-byte codes (uint8)"), _fmt(q_fmt),
+        call.opt(mean, "mean", (rows,), _F32, "float32"), call.opt(rstd, "rstd", (rows,), _F32, "float32")), stream)
+
+
+def te_norm_backward_workspace_size(rows: int, cols: int) -> int:
+    return int(_lib.te_norm_backward_workspace_size(int(rows), int(cols)))
+
+
+def te_norm_backward(kind, dy, x, gamma, mean, rstd, dx, dgamma, dbeta=None, dskip=None, workspace=None,
+                     stream=None) -> None:
+    call, k, rows, cols, dt, xd, wdt, wd = _norm_args(kind, x, gamma)
+    full, w = (rows, cols), (cols,)
+    ws, ws_bytes = call.workspace(workspace)
+    call.run("te_norm_backward", (
+        k, call.ptr(dy, "dy", full, xd, xd[0]), call.ptr(x, "x", full, xd, xd[0]),
+        call.opt(dskip, "dskip", full, xd, xd[0]), dt, rows, cols, call.ptr(gamma, "gamma", w, wd, wd[0]), wdt,
+        call.opt(mean, "mean", (rows,), _F32, "float32"), call.ptr(rstd, "rstd", (rows,), _F32, "float32"),
+        call.ptr(dx, "dx", full, xd, xd[0]), call.ptr(dgamma, "dgamma", w, wd, wd[0]),
+        call.opt(dbeta, "dbeta", w, wd, wd[0]), ws, ws_bytes), stream)
+
+
+def _activation(act) -> int:
+    return ACTIVATIONS[act] if isinstance(act, str) else int(act)
+
+
+def _gated_operands(call, a, a_scale, b, b_scale, rows_b):
+    """Addresses of a [M, K], a_scale, b [rows_b, K] and b_scale."""
+    M, K = a.shape
+    kind = "1-byte codes (uint8)"
+    return (call.ptr(a, "a", (M, K), _U8, kind), call.ptr(a_scale, "a_scale", (M, K // 32), _U8, kind),
+            call.ptr(b, "b", (rows_b, K), _U8, kind), call.ptr(b_scale, "b_scale", (rows_b, K // 32), _U8, kind))
+
+
+def te_mxfp8_gated_gemm_workspace_size(M: int, N: int, K: int) -> int:
+    return int(_lib.te_mxfp8_gated_gemm_workspace_size(M, N, K))
+
+
+def te_mxfp8_gated_gemm(a, a_scale, a_fmt, b, b_scale, b_fmt, d, activation="silu", d_scale=None, d_fmt=None,
+                        bias=None, aux=None, workspace=None, stream=None) -> None:
+    """d_fmt None: d is bf16; "e4m3" / "e5m2": d is the MXFP8 operand (d, d_scale)."""
+    call = _Call(a, "a")
+    _require(a.dim() == 2 and b is not None and b.dim() == 2, "a and b must be 2-D")
+    M, K = a.shape
+    _require(b.shape[0] % 2 == 0, "b: expected an even number of rows (gate rows, then up rows)")
+    N = b.shape[0] // 2
+    pa, psa, pb, psb = _gated_operands(call, a, a_scale, b, b_scale, 2 * N)
+    if d_fmt is None:
+        pd, pds, out = call.ptr(d, "d", (M, N), _B16, "bf16 (or its int16 bits)"), None, TE_BF16
+        _require(d_scale is None, "d_scale: only with an MXFP8 d (d_fmt)")
+    else:
+        pd, out = call.ptr(d, "d", (M, N), _U8, "1-byte codes (uint8)"), _fmt(d_fmt)
+        pds = call.ptr(d_scale, "d_scale", (M, N // 32), _U8, "1-byte codes (uint8)")
+    ws, ws_bytes = call.workspace(workspace)
+    call.run("te_mxfp8_gated_gemm", (
+        pa, psa, _fmt(a_fmt), pb, psb, _fmt(b_fmt), M, N, K, _activation(activation), pd, pds, out,
+        call.opt(bias, "bias", (2 * N,), _B16, "bf16 (or its int16 bits)"),
+        call.opt(aux, "aux", (M, 2 * N), _B16, "bf16 (or its int16 bits)"), ws, ws_bytes), stream)
+
+
+def te_mxfp8_dgated_gemm_workspace_size(M: int, N: int, K: int) -> int:
+    return int(_lib.te_mxfp8_dgated_gemm_workspace_size(M, N, K))
+
+
+def te_mxfp8_dgated_gemm(a, a_scale, a_fmt, b, b_scale, b_fmt, aux, d, activation="silu", workspace=None,
+                         stream=None) -> None:
+    call = _Call(a, "a")
+    _require(a.dim() == 2 and b is not None and b.dim() == 2, "a and b must be 2-D")
+    M, K = a.shape
+    N = b.shape[0]
+    pa, psa, pb, psb = _gated_operands(call, a, a_scale, b, b_scale, N)
+    ws, ws_bytes = call.workspace(workspace)
+    call.run("te_mxfp8_dgated_gemm", (
+        pa, psa, _fmt(a_fmt), pb, psb, _fmt(b_fmt), M, N, K, _activation(activation),
+        call.ptr(aux, "aux", (M, 2 * N), _B16, "bf16 (or its int16 bits)"),
+        call.ptr(d, "d", (M, 2 * N), _B16, "bf16 (or its int16 bits)"), ws, ws_bytes), stream)
+
+
+def te_mxfp8_grouped_gated_gemm(m_splits, a, a_scale, a_fmt, b, b_scale, b_fmt, n: int, d, activation="silu",
+                                bias=None, aux=None, stream=None) -> None:
+    call = _Call(a, "a")
+    _require(m_splits is not None and m_splits.dim() == 1, "m_splits: expected a 1-D int32 tensor")
+    _require(a.dim() == 2, "a must be 2-D")
+    G, n = m_splits.numel(), int(n)
+    M, K = a.shape
+    pa, psa, pb, psb = _gated_operands(call, a, a_scale, b, b_scale, G * 2 * n)
+    call.run("te_mxfp8_grouped_gated_gemm", (
+        G, call.ptr(m_splits, "m_splits", (G,), _I32, "int32"), M, pa, psa, _fmt(a_fmt), pb, psb, _fmt(b_fmt), n, K,
+        _activation(activation), call.ptr(d, "d", (M, n), _B16, "bf16 (or its int16 bits)"),
+        call.opt(bias, "bias", (G, 2 * n), _B16, "bf16 (or its int16 bits)"),
+        call.opt(aux, "aux", (M, 2 * n), _B16, "bf16 (or its int16 bits)")), stream)
+
+
+def te_mxfp8_grouped_dgated_gemm(m_splits, a, a_scale, a_fmt, b, b_scale, b_fmt, n: int, aux, d, activation="silu",
+                                 stream=None) -> None:
+    call = _Call(a, "a")
+    _require(m_splits is not None and m_splits.dim() == 1, "m_splits: expected a 1-D int32 tensor")
+    _require(a.dim() == 2, "a must be 2-D")
+    G, n = m_splits.numel(), int(n)
+    M, K = a.shape
+    pa, psa, pb, psb = _gated_operands(call, a, a_scale, b, b_scale, G * n)
+    call.run("te_mxfp8_grouped_dgated_gemm", (
+        G, call.ptr(m_splits, "m_splits", (G,), _I32, "int32"), M, pa, psa, _fmt(a_fmt), pb, psb, _fmt(b_fmt), n, K,
+        _activation(activation), call.ptr(aux, "aux", (M, 2 * n), _B16, "bf16 (or its int16 bits)"),
+        call.ptr(d, "d", (M, 2 * n), _B16, "bf16 (or its int16 bits)")), stream)
 
 
 # ------------------------------------------------------- allocating helpers

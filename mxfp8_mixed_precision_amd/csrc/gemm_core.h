@@ -485,9 +485,11 @@ __device__ __forceinline__ void wait_vmcnt() {
 // for much of a step.  In the big tile the copiers are waves 4-7, one per
 // SIMD, and the other wave of each SIMD keeps the MFMA pipe busy meanwhile
 // (measured: 8192^3 GEMM ~10% faster than with all 8 waves copying).
-template <class LY, int FA, int FB, int SM = SM_MX>
+// OB is Operand, or another B operand type with load_stage / load_scale_block
+// overloads of its own (the gated GEMM's two-part B).
+template <class LY, int FA, int FB, int SM = SM_MX, class OB = Operand>
 __device__ __forceinline__ void mainloop(uint8_t* lds, v4f (&acc)[LY::FRN][LY::FRM], const Operand& A,
-                                         const Operand& B, int64_t K, int wave, int lane) {
+                                         const OB& B, int64_t K, int wave, int lane) {
   const int wm = wave / LY::NWN, wn = wave % LY::NWN;
 #pragma unroll
   for (int i = 0; i < LY::FRN; ++i)

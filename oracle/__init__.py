@@ -43,10 +43,13 @@ from .bgrad import column_sums, column_abs_sums
 from .delayed_scaling import delayed_scaling_step, next_scale, fp8_gemm_per_tensor
 from .blockwise import quantize_1d, quantize_2d, block_gemm, pow2_at_least, e8m0_of
 from .gemm import mx_gemm, gelu_tanh, dgelu_tanh, epilogue, grouped_mx_gemm, within_tolerance, tolerance_bound
+from .norm import norm_forward, norm_backward
+from .gated import activation, activation_grad, gated, gated_grad
 
 __all__ = [
     "E4M3", "E5M2", "FP8Format", "decode", "encode", "e8m0_decode", "format_by_name",
     "block_scale_code", "quantize_rowwise", "quantize_colwise", "dequantize",
     "amax", "current_scale", "cast_current_scaling",
     "mx_gemm", "gelu_tanh", "epilogue", "grouped_mx_gemm", "within_tolerance", "tolerance_bound",
+    "norm_forward", "norm_backward", "activation", "activation_grad", "gated", "gated_grad",
 ]
