@@ -503,7 +503,7 @@ te_status te_norm_backward(te_norm_kind kind, const void* dy, const void* x, con
  *   bias     bf16 [2N], or NULL
  *   aux      bf16 [M, 2N] = P, what the backward needs, or NULL
  *   Shapes: K % 128 == 0, N % 16 == 0, any M >= 0 (single tokens too);
- *   K <= 2^23, 2N and M < 2^31 - 256, 2N K / 32 < 2^31 - 4096.
+ *   K <= 2^23, N <= 2^22, M < 2^31 - 256, 2N K / 32 < 2^31 - 4096.
  *   M == 0 or N == 0 enqueues nothing; K == 0 gives P = bias.
  *   workspace: optional, as te_mxfp8_gemm's (te_mxfp8_gated_gemm_workspace_size
  *   bytes enable the faster path; same results without).

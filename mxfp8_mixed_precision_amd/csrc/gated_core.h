@@ -18,7 +18,6 @@
 #include "gemm_core.h"
 
 namespace temx {
-namespace {
 
 struct GatedParams {
   const uint8_t* a;
@@ -35,6 +34,11 @@ struct GatedParams {
   const int32_t* m_splits;  // grouped only
   int32_t groups;
 };
+
+// The 4-wave tile's launch (gated_gemm4.hip), with the scales rearranged into the workspace.
+te_status launch_gated4(GatedParams p, bool backward, te_dtype fa, te_dtype fb, void* workspace, hipStream_t stream);
+
+namespace {
 
 // ---- activations ------------------------------------------------------------
 
@@ -100,29 +104,29 @@ __device__ __forceinline__ GatedOperand make_gated_operand(const uint8_t* b, con
   return o;
 }
 
-template <class C, int SM>
+template <class C, int SM, bool WAIT>
 __device__ __forceinline__ void load_stage(uint32_t stage, const Operand& A, const GatedOperand& B,
                                            const CopyOffsets& off, int64_t K, int kt, int c) {
   constexpr int kA = C::BM / 8 / C::NCOPY, kB = C::BN / 8 / C::NCOPY;  // slices per copier
 #pragma unroll
   for (int i = 0; i < (kA > kB ? kA : kB); ++i) {
     const int q = c + C::NCOPY * i;
-    if (i < kA) lds_dma16(A.data, stage + q * 1024, off.data, (int)(8 * C::NCOPY * i * K) + kt * BK);
-    if (i < kB) lds_dma16(B.data, stage + C::kOffBData + q * 1024, off.data, (int)(16 * i * K) + kt * BK);
+    if (i < kA) lds_dma16<WAIT>(A.data, stage + q * 1024, off.data, (int)(8 * C::NCOPY * i * K) + kt * BK);
+    if (i < kB) lds_dma16<WAIT>(B.data, stage + C::kOffBData + q * 1024, off.data, (int)(16 * i * K) + kt * BK);
   }
   if constexpr (C::SB == 1) {
 #pragma unroll
     for (int i = 0; i < C::kScaleSlicesPerCopier; ++i) {
       const int q = c + C::NCOPY * i, s64 = q >> 1;
       if (q & 1)
-        lds_dma4(B.scale, stage + C::kOffBScale + s64 * 256, B.voff_scale, (int)(32 * s64 * (K / 32)) + kt * 4);
+        lds_dma4<WAIT>(B.scale, stage + C::kOffBScale + s64 * 256, B.voff_scale, (int)(32 * s64 * (K / 32)) + kt * 4);
       else
-        lds_dma4(A.scale, stage + C::kOffAScale + s64 * 256, off.scale, (int)(64 * s64 * (K / 32)) + kt * 4);
+        lds_dma4<WAIT>(A.scale, stage + C::kOffAScale + s64 * 256, off.scale, (int)(64 * s64 * (K / 32)) + kt * 4);
     }
   }
 }
 
-template <class C, int SM>
+template <class C, int SM, bool WAIT>
 __device__ __forceinline__ void load_scale_block(uint32_t sbuf, const Operand& A, const GatedOperand& B,
                                                  const CopyOffsets& off, int64_t K, int blk, int c) {
   constexpr int kSa = C::BM / 64, kSb = C::BN / 64;
@@ -132,13 +136,51 @@ __device__ __forceinline__ void load_scale_block(uint32_t sbuf, const Operand& A
     if (q >= kSa + kSb) break;
     const int s64 = q < kSa ? q : q - kSa;
     if (q < kSa)
-      lds_dma16(A.scale, sbuf + s64 * 1024, off.scale, (int)(64 * s64 * (K / 32)) + 16 * blk);
+      lds_dma16<WAIT>(A.scale, sbuf + s64 * 1024, off.scale, (int)(64 * s64 * (K / 32)) + 16 * blk);
     else
-      lds_dma16(B.scale, sbuf + C::BM * 16 + s64 * 1024, B.voff_scale, (int)(32 * s64 * (K / 32)) + 16 * blk);
+      lds_dma16<WAIT>(B.scale, sbuf + C::BM * 16 + s64 * 1024, B.voff_scale, (int)(32 * s64 * (K / 32)) + 16 * blk);
   }
 }
 
+// The 4-wave tile's: copy t of wave w is B slice 8 w + t of the tile, rows
+// 32 w + 16 (t / 4) + 8 (t & 1) of the gate (t / 2 even) or up part.  The
+// lane offsets hold 64 w rows (A's rows), so both resources start 32 w rows
+// early; copies 2, 3, 6 and 7, all up, have 2 KB of their LDS slot in the
+// immediate, which moves the global address too: that resource starts 2 KB
+// earlier still, and the offset takes only the odd copies' 1 KB back.
+// No lane's offset falls below what was taken off the base.
+struct GatedOperand4 {
+  i32x4 data;
+  i32x4 up;
+  i32x4 scale;  // both parts' rows in tile order (gated_scale_blocks_kernel)
+};
+
+__device__ __forceinline__ const i32x4& copy4_b_rsrc(const GatedOperand4& B, int t) { return (t & 2) ? B.up : B.data; }
+__device__ __forceinline__ int copy4_b_soff(const GatedOperand4&, int t, int K) {
+  return (16 * (t >> 2) + 8 * (t & 1)) * K - (t & 1) * 1024;
+}
+
+__device__ __forceinline__ GatedOperand4 make_gated_operand4(const uint8_t* b, const uint8_t* b_scale, int64_t n0,
+                                                             int64_t N, int64_t K, int wave) {
+  const int64_t bytes = min((int64_t)Big4::BN / 2, N - n0) * K, early = 32 * wave * K, nblk = K / 512;
+  GatedOperand4 o;
+  o.data = make_rsrc(b + n0 * K - early, bytes + early);
+  o.up = make_rsrc(b + (N + n0) * K - early - 2048, bytes + early + 2048);
+  o.scale = make_rsrc(b_scale + 2 * n0 * 16, (nblk * 2 * N - 2 * n0) * 16);
+  return o;
+}
+
 // ---- epilogues --------------------------------------------------------------
+//
+// Results leave through LDS: a wave writes blocks of 16-row fragments to a
+// region of its own in rows of 16-byte chunks (chunk c of row q at
+// c ^ (q % chunks), which keeps the 8-byte fragment accesses and the 16-byte
+// row accesses free of bank conflicts), reads them back row-major and stores
+// whole lines.  Stored straight from the MFMA layout an instruction writes 32
+// bytes of each of 16 rows.  A region is 16 KB; LDS accesses of one wave
+// complete in order, so a region needs no barrier of its own.
+constexpr int kRegion = 16 * 1024;
+constexpr int kOutOfRange = (int)0x80000000u;  // a buffer offset past every tile's rows (at most 2^31 bytes)
 
 __device__ __forceinline__ void bf16x4(uint2 v, float (&f)[4]) {
   f[0] = bf16_bits_to_float(v.x & 0xFFFFu);
@@ -151,123 +193,236 @@ __device__ __forceinline__ uint2 pack4(const float (&f)[4]) {
   return make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
 }
 
+// Lane (g, r)'s 8 bytes of fragment column chunk pair `pair` (16 columns = chunks 2 pair, 2 pair + 1) in row
+// 16 jj + r of a region with CH chunks per row.
+template <int CH>
+__device__ __forceinline__ int frag_off(int jj, int pair, int g, int r) {
+  const int q = 16 * jj + r, chunk = 2 * pair + (g >> 1);
+  return q * CH * 16 + ((chunk ^ (q & (CH - 1))) << 4) + ((g & 1) << 3);
+}
+
+// Rows mb .. mb + rows - 1 (below m_end) of a row-major tensor as a buffer resource: accesses past them are
+// dropped or read zeros.  `off` is a lane's offset: row lane / CH and 16-byte chunk lane % CH of a region's rows
+// (UNIT bytes of the tensor per chunk; in TWO-part rows the second CH / 2 chunks lie `half` bytes further on), out
+// of range where its columns are not below N.
+struct RowBuffer {
+  __amdgpu_buffer_rsrc_t rsrc;
+  int off;
+  int stride;  // bytes
+};
+
+template <int CH, int UNIT, bool TWO>
+__device__ __forceinline__ RowBuffer row_buffer(const void* t, int64_t stride, int64_t half, int64_t mb, int64_t m_end,
+                                                int rows, int64_t nb, int64_t N, int lane) {
+  constexpr int CC = TWO ? CH / 2 : CH;
+  const int64_t valid = m_end - mb < 0 ? 0 : (m_end - mb < rows ? m_end - mb : rows);
+  const uint64_t base = reinterpret_cast<uint64_t>(t) + mb * stride;
+  const uint64_t uniform = (uint64_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)base) & 0xFFFFFFFFu;
+  const uint64_t upper = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(base >> 32)) << 32;
+  RowBuffer r;
+  r.rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(upper | uniform), 0,
+                                             __builtin_amdgcn_readfirstlane((int)(valid * stride)), kRsrcWord3);
+  const int c = lane % CH;
+  const int64_t n = nb + 8 * (c % CC);  // N % 16 == 0: a chunk's 8 columns are all in or all out
+  r.off = n < N ? (int)((lane / CH) * stride + (n / 8) * UNIT + (TWO && c >= CC ? half : 0)) : kOutOfRange;
+  r.stride = (int)stride;
+  return r;
+}
+
+template <int CH>
+__device__ __forceinline__ int region_off(int t, int lane) {
+  const int q = (64 * t + lane) / CH, c = lane % CH;
+  return q * CH * 16 + ((c ^ (q & (CH - 1))) << 4);
+}
+
+// ROWS rows x CH chunks of a region to the buffer's rows row0 ..
+template <int CH, int ROWS>
+__device__ __forceinline__ void store_rows(const uint8_t* region, const RowBuffer& to, int row0, int lane) {
+#pragma unroll
+  for (int t = 0; t < ROWS * CH / 64; ++t) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(region + region_off<CH>(t, lane));
+    __builtin_amdgcn_raw_buffer_store_b128(v, to.rsrc, to.off, (row0 + t * (64 / CH)) * to.stride, 0);
+  }
+}
+
+// The same region of bf16 values as MXFP8 codes and scales (the buffers' chunks are 8 codes; scales: one byte for
+// every 4 chunks): the four lanes of a DPP quad read a row's 32-block.
+template <int CH, int ROWS, int FMT>
+__device__ __forceinline__ void store_rows_mx(const uint8_t* region, const RowBuffer& to, const RowBuffer& scales,
+                                              int row0, int lane) {
+#pragma unroll
+  for (int t = 0; t < ROWS * CH / 64; ++t) {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(region + region_off<CH>(t, lane));
+    const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
+    const uint32_t code = e8m0_code_from_amax_bits<FMT>(quad_max(absmax_bits8(v)));
+    const uint2 x = cvt8_scaled<FMT>(v, e8m0_to_float(code));
+    const int row = row0 + t * (64 / CH);
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{x.x, x.y}, to.rsrc, to.off, row * to.stride, 0);
+    if ((lane & 3) == 0)
+      __builtin_amdgcn_raw_buffer_store_b8((uint8_t)code, scales.rsrc, scales.off, row * scales.stride, 0);
+  }
+}
+
+// AGPR accumulators (the 4-wave tile) are read fragment by fragment: the empty asm statement keeps the compiler
+// from pulling all 256 into VGPRs at once.
+template <class LY>
+constexpr bool in_agprs() { return LY::FRN * LY::FRM > 32; }
+
 // Forward: fragments 2 p (gate) and 2 p + 1 (up) hold columns n0 + (WTN / 2) wn + 16 p + 4 g + e.
-template <class LY, int ACT, int OUT>
-__device__ __forceinline__ void epilogue_gated(v4f (&acc)[LY::FRN][LY::FRM], const GatedParams& p,
+template <class LY>
+__device__ __forceinline__ void epilogue_gated(v4f (&acc)[LY::FRN][LY::FRM], uint8_t* lds, const GatedParams& p,
                                                const uint16_t* bias, int64_t m0, int64_t m_end, int64_t n0, int wave,
                                                int lane) {
-  constexpr int NP = LY::FRN / 2;
+  constexpr int NP = LY::FRN / 2, CW = LY::WTN / 2, CHD = CW / 8, FRH = 4, ROWS = 16 * FRH;
+  static_assert(ROWS * CHD * 2 * 16 <= kRegion && LY::FRM % FRH == 0 && (CHD & (CHD - 1)) == 0, "staging layout");
   const int wm = wave / LY::NWN, wn = wave % LY::NWN;
   const int g = lane >> 4, r = lane & 15;
-  const int64_t N = p.N, nw = n0 + wn * (LY::WTN / 2) + 4 * g;
-  if (bias != nullptr) {
+  const int64_t N = p.N, mw = m0 + wm * LY::WTM, nw = n0 + wn * CW;
+  uint8_t* region = lds + wave * (ROWS * CHD * 2 * 16);
+  // the bias goes in place where the accumulators are VGPRs; AGPR ones take it as they are read
+  float bv[in_agprs<LY>() ? LY::FRN : 1][4];
 #pragma unroll
-    for (int i = 0; i < LY::FRN; ++i) {
-      const int64_t n = nw + 16 * (i >> 1);
-      float b[4];
+  for (int i = 0; i < LY::FRN; ++i) {
+    float b[4] = {0.f, 0.f, 0.f, 0.f};
+    if (bias != nullptr) {
+      const int64_t n = nw + 16 * (i >> 1) + 4 * g;  // columns past N (never stored) read column 0's
       bf16x4(*reinterpret_cast<const uint2*>(bias + (n < N ? n : 0) + (i & 1) * N), b);
+    }
+    if constexpr (in_agprs<LY>()) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) bv[i][e] = b[e];
+    } else if (bias != nullptr) {
 #pragma unroll
       for (int j = 0; j < LY::FRM; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][j][e] += b[e];
     }
   }
+  auto read = [&](int i, int j, float (&f)[4]) __attribute__((always_inline)) {
+    if constexpr (in_agprs<LY>()) asm volatile("" : "+a"(acc[i][j]));
 #pragma unroll
-  for (int j = 0; j < LY::FRM; ++j) {
-    const int64_t m = m0 + wm * LY::WTM + 16 * j + r;
-    const bool row_ok = m < m_end;
-    uint2 bits[NP];
-#pragma unroll
-    for (int q = 0; q < NP; ++q) {
-      const int64_t n = nw + 16 * q;
-      float ga[4], up[4], v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        ga[e] = acc[2 * q][j][e];
-        up[e] = acc[2 * q + 1][j][e];
-        v[e] = act_value<ACT>(ga[e]) * up[e];
-      }
-      bits[q] = pack4(v);
-      if (row_ok && n < N) {
-        if (p.aux != nullptr) {
-          *reinterpret_cast<uint2*>(p.aux + m * 2 * N + n) = pack4(ga);
-          *reinterpret_cast<uint2*>(p.aux + m * 2 * N + N + n) = pack4(up);
-        }
-        if constexpr (OUT == TE_BF16) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.d) + m * N + n) = bits[q];
-      }
+    for (int e = 0; e < 4; ++e) {
+      f[e] = acc[i][j][e];
+      if constexpr (in_agprs<LY>()) f[e] += bv[i][e];
     }
-    if constexpr (OUT != TE_BF16) {
-      // MXFP8: the bf16 values in 32-column blocks, two fragment pairs each; lanes g = 0..3 of a row hold
-      // a block's columns 4 g .. 4 g + 3 and 16 + 4 g .. 16 + 4 g + 3
-      static_assert(NP % 2 == 0, "a 32-column block is two fragment pairs of one wave");
+  };
+  const bool mx = p.out != TE_BF16;
+  const RowBuffer to_d = mx ? row_buffer<CHD, 8, false>(p.d, N, 0, mw, m_end, LY::WTM, nw, N, lane)
+                            : row_buffer<CHD, 16, false>(p.d, 2 * N, 0, mw, m_end, LY::WTM, nw, N, lane);
+  __syncthreads();  // every wave's reads of the last stage are done: the LDS is free
 #pragma unroll
-      for (int b = 0; b < NP / 2; ++b) {
-        const int64_t nb = n0 + wn * (LY::WTN / 2) + 32 * b;
-        const uint4 v = make_uint4(bits[2 * b].x, bits[2 * b].y, bits[2 * b + 1].x, bits[2 * b + 1].y);
-        uint32_t amax = absmax_bits8(v);
-        amax = max(amax, (uint32_t)__builtin_amdgcn_ds_swizzle((int)amax, 0x401F));           // lane ^ 16
-        amax = max(amax, (uint32_t)__builtin_amdgcn_ds_bpermute((lane ^ 32) << 2, (int)amax));  // lane ^ 32
-        const uint32_t code = e8m0_code_from_amax_bits<OUT>(amax);
-        const uint2 c = cvt8_scaled<OUT>(v, e8m0_to_float(code));
-        if (row_ok && nb < p.N) {
-          uint8_t* d = static_cast<uint8_t*>(p.d) + m * N + nb + 4 * g;
-          *reinterpret_cast<uint32_t*>(d) = c.x;
-          *reinterpret_cast<uint32_t*>(d + 16) = c.y;
-          if (g == 0) p.d_scale[m * (N / 32) + nb / 32] = (uint8_t)code;
+  for (int h = 0; h < LY::FRM / FRH; ++h) {
+    if (p.aux != nullptr) {
+#pragma unroll
+      for (int jj = 0; jj < FRH; ++jj)
+#pragma unroll
+        for (int i = 0; i < LY::FRN; ++i) {
+          float f[4];
+          read(i, FRH * h + jj, f);
+          *reinterpret_cast<uint2*>(region + frag_off<2 * CHD>(jj, (i >> 1) + (i & 1) * NP, g, r)) = pack4(f);
         }
-      }
+      asm volatile("" ::: "memory");
+      store_rows<2 * CHD, ROWS>(
+          region, row_buffer<2 * CHD, 16, true>(p.aux, 4 * N, 2 * N, mw, m_end, LY::WTM, nw, N, lane), ROWS * h, lane);
+      asm volatile("" ::: "memory");
     }
+    auto product = [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+      for (int jj = 0; jj < FRH; ++jj)
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+          float ga[4], up[4];
+          read(2 * q, FRH * h + jj, ga);
+          read(2 * q + 1, FRH * h + jj, up);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ga[e] = act_value<decltype(act)::value>(ga[e]) * up[e];
+          *reinterpret_cast<uint2*>(region + frag_off<CHD>(jj, q, g, r)) = pack4(ga);
+        }
+    };
+    if (p.act == TE_ACT_SILU) product(std::integral_constant<int, TE_ACT_SILU>{});
+    else product(std::integral_constant<int, TE_ACT_GELU>{});
+    asm volatile("" ::: "memory");
+    if (!mx) {
+      store_rows<CHD, ROWS>(region, to_d, ROWS * h, lane);
+    } else {
+      // a chunk's scale byte: (n / 32) bytes into its row, so n / 8 chunks of 1 / 4 byte
+      RowBuffer scales = row_buffer<CHD, 4, false>(p.d_scale, N / 32, 0, mw, m_end, LY::WTM, nw, N, lane);
+      if (scales.off != kOutOfRange)
+        scales.off = (lane / CHD) * scales.stride + (int)((nw + 8 * (lane % CHD)) / 32);
+      if (p.out == TE_E4M3) store_rows_mx<CHD, ROWS, TE_E4M3>(region, to_d, scales, ROWS * h, lane);
+      else store_rows_mx<CHD, ROWS, TE_E5M2>(region, to_d, scales, ROWS * h, lane);
+    }
+    asm volatile("" ::: "memory");
   }
 }
 
-template <class LY, int ACT>
-__device__ __forceinline__ void epilogue_dgated(v4f (&acc)[LY::FRN][LY::FRM], const GatedParams& p, int64_t m0,
-                                                int64_t m_end, int64_t n0, int wave, int lane) {
+// Backward: fragment i holds columns n0 + WTN wn + 16 i + 4 g + e of acc; blocks of rows of aux come through the
+// region the same way the gradients leave (row = gate chunks, then up chunks).
+template <class LY>
+__device__ __forceinline__ void epilogue_dgated(v4f (&acc)[LY::FRN][LY::FRM], uint8_t* lds, const GatedParams& p,
+                                                int64_t m0, int64_t m_end, int64_t n0, int wave, int lane) {
+  constexpr int CH = LY::WTN / 4, FRH = 1, ROWS = 16 * FRH;
+  constexpr int kT = ROWS * CH / 64;  // 16-byte accesses per lane and block
+  static_assert((CH & (CH - 1)) == 0, "staging layout");
   const int wm = wave / LY::NWN, wn = wave % LY::NWN;
   const int g = lane >> 4, r = lane & 15;
-  const int64_t N = p.N;
+  const int64_t N = p.N, mw = m0 + wm * LY::WTM, nw = n0 + wn * LY::WTN;
+  uint8_t* region = lds + wave * (ROWS * CH * 16);
+  const RowBuffer from = row_buffer<CH, 16, true>(p.aux, 4 * N, 2 * N, mw, m_end, LY::WTM, nw, N, lane);
+  const RowBuffer to = row_buffer<CH, 16, true>(p.d, 4 * N, 2 * N, mw, m_end, LY::WTM, nw, N, lane);
+  u32x4 v[kT];
+  auto load = [&](int h) __attribute__((always_inline)) {
 #pragma unroll
-  for (int j = 0; j < LY::FRM; ++j) {
-    const int64_t m = m0 + wm * LY::WTM + 16 * j + r;
-    if (m >= m_end) continue;
+    for (int t = 0; t < kT; ++t)
+      v[t] = __builtin_amdgcn_raw_buffer_load_b128(from.rsrc, from.off, (ROWS * h + t * (64 / CH)) * from.stride, 0);
+  };
+  load(0);
+  __syncthreads();  // every wave's reads of the last stage are done: the LDS is free
 #pragma unroll
-    for (int i = 0; i < LY::FRN; ++i) {
-      const int64_t n = n0 + wn * LY::WTN + 16 * i + 4 * g;
-      if (n >= N) continue;
-      float ga[4], up[4];
-      bf16x4(*reinterpret_cast<const uint2*>(p.aux + m * 2 * N + n), ga);
-      bf16x4(*reinterpret_cast<const uint2*>(p.aux + m * 2 * N + N + n), up);
+  for (int h = 0; h < LY::FRM / FRH; ++h) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float v, dv;
-        act_and_grad<ACT>(ga[e], v, dv);
-        ga[e] = acc[i][j][e] * up[e] * dv;
-        up[e] = acc[i][j][e] * v;
-      }
-      uint16_t* d = static_cast<uint16_t*>(p.d) + m * 2 * N + n;
-      *reinterpret_cast<uint2*>(d) = pack4(ga);
-      *reinterpret_cast<uint2*>(d + N) = pack4(up);
-    }
+    for (int t = 0; t < kT; ++t) *reinterpret_cast<u32x4*>(region + region_off<CH>(t, lane)) = v[t];
+    if (h + 1 < LY::FRM / FRH) load(h + 1);  // in flight while this block is computed
+    asm volatile("" ::: "memory");
+    auto gradients = [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+      for (int jj = 0; jj < FRH; ++jj)
+#pragma unroll
+        for (int i = 0; i < LY::FRN; ++i) {
+          const int j = FRH * h + jj;
+          if constexpr (in_agprs<LY>()) asm volatile("" : "+a"(acc[i][j]));
+          uint2* pg = reinterpret_cast<uint2*>(region + frag_off<CH>(jj, i, g, r));
+          uint2* pu = reinterpret_cast<uint2*>(region + frag_off<CH>(jj, LY::FRN + i, g, r));
+          float ga[4], up[4];
+          bf16x4(*pg, ga);
+          bf16x4(*pu, up);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float a = acc[i][j][e];
+            float f, df;
+            act_and_grad<decltype(act)::value>(ga[e], f, df);
+            ga[e] = a * up[e] * df;
+            up[e] = a * f;
+          }
+          *pg = pack4(ga);
+          *pu = pack4(up);
+        }
+    };
+    if (p.act == TE_ACT_SILU) gradients(std::integral_constant<int, TE_ACT_SILU>{});
+    else gradients(std::integral_constant<int, TE_ACT_GELU>{});
+    asm volatile("" ::: "memory");
+    store_rows<CH, ROWS>(region, to, ROWS * h, lane);
+    asm volatile("" ::: "memory");
   }
 }
 
 // A tile's accumulators to D (and aux / MXFP8 scales).
 template <class LY, bool BWD>
-__device__ __forceinline__ void finish_gated(v4f (&acc)[LY::FRN][LY::FRM], const GatedParams& p,
+__device__ __forceinline__ void finish_gated(v4f (&acc)[LY::FRN][LY::FRM], uint8_t* lds, const GatedParams& p,
                                              const uint16_t* bias, int64_t m0, int64_t m_end, int64_t n0, int wave,
                                              int lane) {
-  auto with_act = [&](auto act) __attribute__((always_inline)) {
-    constexpr int ACT = decltype(act)::value;
-    if constexpr (BWD) {
-      epilogue_dgated<LY, ACT>(acc, p, m0, m_end, n0, wave, lane);
-    } else {
-      if (p.out == TE_BF16) epilogue_gated<LY, ACT, TE_BF16>(acc, p, bias, m0, m_end, n0, wave, lane);
-      else if (p.out == TE_E4M3) epilogue_gated<LY, ACT, TE_E4M3>(acc, p, bias, m0, m_end, n0, wave, lane);
-      else epilogue_gated<LY, ACT, TE_E5M2>(acc, p, bias, m0, m_end, n0, wave, lane);
-    }
-  };
-  if (p.act == TE_ACT_SILU) with_act(std::integral_constant<int, TE_ACT_SILU>{});
-  else with_act(std::integral_constant<int, TE_ACT_GELU>{});
+  if constexpr (BWD) epilogue_dgated<LY>(acc, lds, p, m0, m_end, n0, wave, lane);
+  else epilogue_gated<LY>(acc, lds, p, bias, m0, m_end, n0, wave, lane);
 }
 
 // Output columns of a tile: a forward tile's B rows are gate and up rows of BN / 2 columns.
@@ -283,12 +438,12 @@ __device__ __forceinline__ void gated_tile(uint8_t* lds, const GatedParams& p, c
   v4f acc[LY::FRN][LY::FRM];
   if constexpr (BWD) {
     const Operand B = make_operand(b, b_scale, n0, p.N - n0, p.K, LY::BN);
-    mainloop<LY, FA, FB>(lds, acc, A, B, p.K, wave, lane);
+    mainloop<LY, FA, FB, SM_MX, true>(lds, acc, A, B, p.K, wave, lane);
   } else {
     const GatedOperand B = make_gated_operand<LY>(b, b_scale, n0, p.N, p.K, wave, lane);
-    mainloop<LY, FA, FB>(lds, acc, A, B, p.K, wave, lane);
+    mainloop<LY, FA, FB, SM_MX, true>(lds, acc, A, B, p.K, wave, lane);
   }
-  finish_gated<LY, BWD>(acc, p, bias, m0, m_end, n0, wave, lane);
+  finish_gated<LY, BWD>(acc, lds, p, bias, m0, m_end, n0, wave, lane);
 }
 
 template <class LY, int FA, int FB, bool BWD>

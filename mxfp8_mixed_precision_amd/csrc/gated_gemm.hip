@@ -32,11 +32,29 @@ te_status launch_grouped_gated(const GatedParams& p, te_dtype fa, te_dtype fb, u
 }
 
 // Shape limits: those of the dense GEMMs with the 2N rows of the forward's weights, whose scales are addressed
-// with 32-bit offsets.
+// with 32-bit offsets, as are 128 rows of 2N bf16 pre-activations.
 bool gated_shape_ok(int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N < 0 || K < 0 || K % 128 != 0 || N % 16 != 0) return false;
-  if (N > ((int64_t)1 << 30) - 256 || !dense_shape_ok(M, 2 * N, K)) return false;
+  if (N > ((int64_t)1 << 22) || !dense_shape_ok(M, 2 * N, K)) return false;
   return 2 * N * (K / 32) < ((int64_t)1 << 31) - 4096;
+}
+
+// Workspace of the 4-wave tile: the rearranged scales of A and of B's `cols` rows; 0 where it does not serve.
+size_t gated_workspace(int64_t M, int64_t cols, int64_t K, int64_t N) {
+  if (M <= 0 || N <= 0 || K <= 0 || !gated_shape_ok(M, N, K)) return 0;
+  return four_wave_mx(M, cols, K) ? scale_blocks_bytes(M, cols, K) : 0;
+}
+
+template <bool BWD>
+te_status dense_gated(const GatedParams& p, te_dtype fa, te_dtype fb, void* workspace, size_t workspace_bytes,
+                      hipStream_t stream) {
+  const int64_t cols = BWD ? p.N : 2 * p.N;
+  const size_t want = gated_workspace(p.M, cols, p.K, p.N);
+  if (want > 0 && workspace != nullptr && workspace_bytes >= want && ((uintptr_t)workspace & 255u) == 0 &&
+      aligned16(p.a_scale) && aligned16(p.b_scale))
+    return launch_gated4(p, BWD, fa, fb, workspace, stream);
+  if (use_small_tile(((p.M + 255) / 256) * ((cols + 255) / 256))) return launch_gated<Small, BWD>(p, fa, fb, stream);
+  return launch_gated<Big, BWD>(p, fa, fb, stream);
 }
 
 te_status check_operands(const uint8_t* a, const uint8_t* a_scale, const uint8_t* b, const uint8_t* b_scale) {
@@ -58,10 +76,7 @@ te_status check_formats(te_dtype a_fmt, te_dtype b_fmt, te_activation act) {
 using namespace temx;
 
 extern "C" size_t te_mxfp8_gated_gemm_workspace_size(int64_t M, int64_t N, int64_t K) {
-  (void)M;
-  (void)N;
-  (void)K;
-  return 0;
+  return gated_workspace(M, 2 * N, K, N);
 }
 
 extern "C" te_status te_mxfp8_gated_gemm(const uint8_t* a, const uint8_t* a_scale, te_dtype a_fmt, const uint8_t* b,
@@ -69,8 +84,6 @@ extern "C" te_status te_mxfp8_gated_gemm(const uint8_t* a, const uint8_t* a_scal
                                          te_activation act, void* d, uint8_t* d_scale, te_dtype d_dtype,
                                          const uint16_t* bias, uint16_t* aux, void* workspace, size_t workspace_bytes,
                                          hipStream_t stream) {
-  (void)workspace;
-  (void)workspace_bytes;
   te_status st = check_formats(a_fmt, b_fmt, act);
   if (st != TE_OK) return st;
   TE_REQUIRE(d_dtype == TE_BF16 || is_fp8(d_dtype), TE_ERR_DTYPE);
@@ -83,22 +96,17 @@ extern "C" te_status te_mxfp8_gated_gemm(const uint8_t* a, const uint8_t* a_scal
   if (K > 0 && (st = check_operands(a, a_scale, b, b_scale)) != TE_OK) return st;
   TE_REQUIRE(device_is_gfx950(), TE_ERR_ARCH);
   const GatedParams p{a, a_scale, b, b_scale, d, d_scale, bias, aux, M, N, K, act, d_dtype, nullptr, 0};
-  return launch_gated<Small, false>(p, a_fmt, b_fmt, stream);
+  return dense_gated<false>(p, a_fmt, b_fmt, workspace, workspace_bytes, stream);
 }
 
 extern "C" size_t te_mxfp8_dgated_gemm_workspace_size(int64_t M, int64_t N, int64_t K) {
-  (void)M;
-  (void)N;
-  (void)K;
-  return 0;
+  return gated_workspace(M, N, K, N);
 }
 
 extern "C" te_status te_mxfp8_dgated_gemm(const uint8_t* a, const uint8_t* a_scale, te_dtype a_fmt, const uint8_t* b,
                                           const uint8_t* b_scale, te_dtype b_fmt, int64_t M, int64_t N, int64_t K,
                                           te_activation act, const uint16_t* aux, uint16_t* d, void* workspace,
                                           size_t workspace_bytes, hipStream_t stream) {
-  (void)workspace;
-  (void)workspace_bytes;
   te_status st = check_formats(a_fmt, b_fmt, act);
   if (st != TE_OK) return st;
   TE_REQUIRE(gated_shape_ok(M, N, K), TE_ERR_SHAPE);
@@ -109,7 +117,7 @@ extern "C" te_status te_mxfp8_dgated_gemm(const uint8_t* a, const uint8_t* a_sca
   TE_REQUIRE(device_is_gfx950(), TE_ERR_ARCH);
   const GatedParams p{a, a_scale, b,  b_scale, d,   nullptr, nullptr, const_cast<uint16_t*>(aux),
                       M, N,       K,  act,     TE_BF16, nullptr, 0};
-  return launch_gated<Small, true>(p, a_fmt, b_fmt, stream);
+  return dense_gated<true>(p, a_fmt, b_fmt, workspace, workspace_bytes, stream);
 }
 
 namespace temx {
@@ -133,7 +141,10 @@ te_status grouped_gated(GatedParams p, te_dtype a_fmt, te_dtype b_fmt, hipStream
   TE_REQUIRE(device_is_gfx950(), TE_ERR_ARCH);
   const int cus = device_cu_count();
   const unsigned grid = cus < 8 ? 8u : (unsigned)(cus / 8 * 8);
-  return launch_grouped_gated<Small, BWD>(p, a_fmt, b_fmt, 2 * grid, stream);
+  // the splits stay on the device: the big-tile count is estimated from the total rows, one ragged tail per group
+  if (use_small_tile((p.M / 256 + p.groups) * ((cols + 255) / 256)))
+    return launch_grouped_gated<Small, BWD>(p, a_fmt, b_fmt, 2 * grid, stream);
+  return launch_grouped_gated<Big, BWD>(p, a_fmt, b_fmt, grid, stream);
 }
 
 }  // namespace

@@ -207,8 +207,25 @@ __device__ __forceinline__ Operand make_operand_2d(const uint8_t* data, const ui
 // stage being read, does not wait for them before every LDS read; the K loop
 // orders them itself (s_waitcnt vmcnt(0) + barrier before a stage is read).
 // m0 is saved and restored around the copy (the LDS base is read at issue).
+// WAIT: 5 wait states between whatever precedes and the copy, as a VALU write
+// of one of its SGPRs needs (v_readlane / v_readfirstlane; the compiler cannot
+// insert them ahead of an asm statement): for kernels whose SGPR pressure
+// makes the compiler keep a resource or offset in VGPR lanes.
+template <bool WAIT = false>
 __device__ __forceinline__ void lds_dma16(const i32x4& rsrc, uint32_t lds_addr, int voff, int soff) {
   int saved;
+  if constexpr (WAIT) {
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %1\n\t"
+        "s_nop 2\n\t"
+        "buffer_load_dwordx4 %2, %3, %4 offen lds\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff)
+        : "memory");
+    return;
+  }
   asm volatile(
       "s_mov_b32 %0, m0\n\t"
       "s_mov_b32 m0, %1\n\t"
@@ -219,8 +236,21 @@ __device__ __forceinline__ void lds_dma16(const i32x4& rsrc, uint32_t lds_addr, 
       : "memory");
 }
 
+template <bool WAIT = false>
 __device__ __forceinline__ void lds_dma4(const i32x4& rsrc, uint32_t lds_addr, int voff, int soff) {
   int saved;
+  if constexpr (WAIT) {
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %1\n\t"
+        "s_nop 2\n\t"
+        "buffer_load_dword %2, %3, %4 offen lds\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff)
+        : "memory");
+    return;
+  }
   asm volatile(
       "s_mov_b32 %0, m0\n\t"
       "s_mov_b32 m0, %1\n\t"
@@ -254,7 +284,7 @@ __device__ __forceinline__ CopyOffsets copy_offsets(int64_t K, int c, int lane) 
   return o;
 }
 
-template <class C, int SM = SM_MX>
+template <class C, int SM = SM_MX, bool WAIT = false>
 __device__ __forceinline__ void load_stage(uint32_t stage, const Operand& A, const Operand& B,
                                            const CopyOffsets& off, int64_t K, int kt, int c) {
   constexpr int kA = C::BM / 8 / C::NCOPY, kB = C::BN / 8 / C::NCOPY;  // slices per copier
@@ -262,8 +292,8 @@ __device__ __forceinline__ void load_stage(uint32_t stage, const Operand& A, con
   for (int i = 0; i < (kA > kB ? kA : kB); ++i) {
     const int q = c + C::NCOPY * i;
     const int so = (int)(8 * C::NCOPY * i * K) + kt * BK;
-    if (i < kA) lds_dma16(A.data, stage + q * 1024, off.data, so);
-    if (i < kB) lds_dma16(B.data, stage + C::kOffBData + q * 1024, off.data, so);
+    if (i < kA) lds_dma16<WAIT>(A.data, stage + q * 1024, off.data, so);
+    if (i < kB) lds_dma16<WAIT>(B.data, stage + C::kOffBData + q * 1024, off.data, so);
   }
   if constexpr (SM != SM_PT && C::SB == 1) {
 #pragma unroll
@@ -272,11 +302,11 @@ __device__ __forceinline__ void load_stage(uint32_t stage, const Operand& A, con
       const int slice_off = (int)(64 * s64 * (K / 32)) + kt * 4;
       if (q & 1) {
         if constexpr (b_2d(SM))  // the 64 rows lie in 128-row block s64 / 2: one scale row for all lanes
-          lds_dma4(B.scale, stage + C::kOffBScale + s64 * 256, 0, (int)((s64 >> 1) * (K / 32)) + kt * 4);
+          lds_dma4<WAIT>(B.scale, stage + C::kOffBScale + s64 * 256, 0, (int)((s64 >> 1) * (K / 32)) + kt * 4);
         else
-          lds_dma4(B.scale, stage + C::kOffBScale + s64 * 256, off.scale, slice_off);
+          lds_dma4<WAIT>(B.scale, stage + C::kOffBScale + s64 * 256, off.scale, slice_off);
       } else {
-        lds_dma4(A.scale, stage + C::kOffAScale + s64 * 256, off.scale, slice_off);
+        lds_dma4<WAIT>(A.scale, stage + C::kOffAScale + s64 * 256, off.scale, slice_off);
       }
     }
   }
@@ -287,7 +317,7 @@ __device__ __forceinline__ void load_stage(uint32_t stage, const Operand& A, con
 // the 2 BM / 64 is copied by copier q % NCOPY, lane l landing at row 64 s + l.
 // With 2-D B blocks (b_2d) a B slice's 64 rows all take their 128-row block
 // row's scales.
-template <class C, int SM>
+template <class C, int SM, bool WAIT = false>
 __device__ __forceinline__ void load_scale_block(uint32_t sbuf, const Operand& A, const Operand& B,
                                                  const CopyOffsets& off, int64_t K, int blk, int c) {
   constexpr int kSa = C::BM / 64, kSb = C::BN / 64;  // slices of A, then of B
@@ -298,11 +328,11 @@ __device__ __forceinline__ void load_scale_block(uint32_t sbuf, const Operand& A
     const int s64 = q < kSa ? q : q - kSa;
     const int soff = (int)(64 * s64 * (K / 32)) + 16 * blk;
     if (q < kSa) {
-      lds_dma16(A.scale, sbuf + s64 * 1024, off.scale, soff);
+      lds_dma16<WAIT>(A.scale, sbuf + s64 * 1024, off.scale, soff);
     } else if constexpr (b_2d(SM)) {
-      lds_dma16(B.scale, sbuf + C::BM * 16 + s64 * 1024, 0, (int)((s64 >> 1) * (K / 32)) + 16 * blk);
+      lds_dma16<WAIT>(B.scale, sbuf + C::BM * 16 + s64 * 1024, 0, (int)((s64 >> 1) * (K / 32)) + 16 * blk);
     } else {
-      lds_dma16(B.scale, sbuf + C::BM * 16 + s64 * 1024, off.scale, soff);
+      lds_dma16<WAIT>(B.scale, sbuf + C::BM * 16 + s64 * 1024, off.scale, soff);
     }
   }
 }
@@ -486,8 +516,8 @@ __device__ __forceinline__ void wait_vmcnt() {
 // SIMD, and the other wave of each SIMD keeps the MFMA pipe busy meanwhile
 // (measured: 8192^3 GEMM ~10% faster than with all 8 waves copying).
 // OB is Operand, or another B operand type with load_stage / load_scale_block
-// overloads of its own (the gated GEMM's two-part B).
-template <class LY, int FA, int FB, int SM = SM_MX, class OB = Operand>
+// overloads of its own (the gated GEMM's two-part B); WAIT as lds_dma16's.
+template <class LY, int FA, int FB, int SM = SM_MX, bool WAIT = false, class OB = Operand>
 __device__ __forceinline__ void mainloop(uint8_t* lds, v4f (&acc)[LY::FRN][LY::FRM], const Operand& A,
                                          const OB& B, int64_t K, int wave, int lane) {
   const int wm = wave / LY::NWN, wn = wave % LY::NWN;
@@ -510,8 +540,8 @@ __device__ __forceinline__ void mainloop(uint8_t* lds, v4f (&acc)[LY::FRN][LY::F
   if (copier) {
 #pragma unroll
     for (int s = 0; s < S - 1; ++s)
-      if (s < kt_n) load_stage<LY, SM>(lds_addr + s * LY::kStage, A, B, off, K, s, c);
-    if constexpr (kBlk) load_scale_block<LY, SM>(lds_addr + LY::kOffScaleBuf, A, B, off, K, 0, c);
+      if (s < kt_n) load_stage<LY, SM, WAIT>(lds_addr + s * LY::kStage, A, B, off, K, s, c);
+    if constexpr (kBlk) load_scale_block<LY, SM, WAIT>(lds_addr + LY::kOffScaleBuf, A, B, off, K, 0, c);
   }
   for (int kt = 0; kt < kt_n; ++kt) {
     // stage kt has landed once at most `ahead` later stages' copies are outstanding
@@ -521,12 +551,12 @@ __device__ __forceinline__ void mainloop(uint8_t* lds, v4f (&acc)[LY::FRN][LY::F
     else __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
     if (copier && kt + S - 1 < kt_n)
-      load_stage<LY, SM>(lds_addr + ((kt + S - 1) % S) * LY::kStage, A, B, off, K, kt + S - 1, c);
+      load_stage<LY, SM, WAIT>(lds_addr + ((kt + S - 1) % S) * LY::kStage, A, B, off, K, kt + S - 1, c);
     if constexpr (kBlk) {
       // block kt / 4 + 1 goes into the buffer block kt / 4 - 1 used, whose last reads precede this barrier
       const int nb = (kt >> 2) + 1;
       if (copier && (kt & 3) == 0 && 4 * nb < kt_n)
-        load_scale_block<LY, SM>(lds_addr + LY::kOffScaleBuf + (nb & 1) * LY::kScaleBuf, A, B, off, K, nb, c);
+        load_scale_block<LY, SM, WAIT>(lds_addr + LY::kOffScaleBuf + (nb & 1) * LY::kScaleBuf, A, B, off, K, nb, c);
       compute<LY, FA, FB, SM>(lds + (kt % S) * LY::kStage, acc, ro,
                               lds + LY::kOffScaleBuf + ((kt >> 2) & 1) * LY::kScaleBuf + 4 * (kt & 3));
     } else {
@@ -645,18 +675,22 @@ __device__ __forceinline__ Copy4 copy4_offsets(int K, int wave, int lane) {
   co.vo_s = 16 * lane;
   return co;
 }
+// B's resource and offset of copy t (less the immediate's part); a B operand type other than Operand brings
+// overloads of its own
+__device__ __forceinline__ const i32x4& copy4_b_rsrc(const Operand& B, int) { return B.data; }
+__device__ __forceinline__ int copy4_b_soff(const Operand&, int t, int K) { return 8 * t * K - (t & 3) * 1024; }
 // data copy c (0..15: A slices, then B) of the K step at byte kbase into the stage at l_stage; copies
 // 0, 4, 8 and 12 set m0, the next three add their immediate offset to it (WAIT: see lds_dma16_imm)
-template <bool WAIT = false>
-__device__ __forceinline__ void copy4_data(const Operand& A, const Operand& B, const Copy4& co, int c, int K,
+template <bool WAIT = false, class OB = Operand>
+__device__ __forceinline__ void copy4_data(const Operand& A, const OB& B, const Copy4& co, int c, int K,
                                            int kbase, uint32_t l_stage, int wave) {
   const int t = c & 7;
   const bool isb = c >= 8;
   if ((t & 3) == 0)
     set_m0((uint32_t)__builtin_amdgcn_readfirstlane((int)(l_stage + (isb ? Big4::kHalf : 0) + (8 * wave + t) * 1024)));
-  const int so = __builtin_amdgcn_readfirstlane(8 * t * K - (t & 3) * 1024) + kbase;
+  const int so = __builtin_amdgcn_readfirstlane(isb ? copy4_b_soff(B, t, K) : 8 * t * K - (t & 3) * 1024) + kbase;
   const int vo = (t & 1) ? co.vo_o : co.vo_e;
-  const i32x4& rs = isb ? B.data : A.data;
+  const i32x4& rs = isb ? copy4_b_rsrc(B, t) : A.data;
   switch (t & 3) {
     case 0: lds_dma16_imm<0, WAIT>(rs, vo, so); break;
     case 1: lds_dma16_imm<1024, WAIT>(rs, vo, so); break;
@@ -666,8 +700,8 @@ __device__ __forceinline__ void copy4_data(const Operand& A, const Operand& B, c
 }
 // scale slice s = wave + 4k of block blk (1 KB: 64 rows of 16 bytes) into the scale buffer at l_sbuf:
 // k = 0 A rows 64 w .., k = 1 B rows 64 w ..  (a_blk / b_blk: the byte offset of one block)
-template <bool WAIT = false>
-__device__ __forceinline__ void copy4_scales(const Operand& A, const Operand& B, const Copy4& co, int blk,
+template <bool WAIT = false, class OB = Operand>
+__device__ __forceinline__ void copy4_scales(const Operand& A, const OB& B, const Copy4& co, int blk,
                                              uint32_t l_sbuf, int k, int wave, int a_blk, int b_blk) {
   const int s = wave + 4 * k;
   blk = __builtin_amdgcn_readfirstlane(blk);
@@ -684,8 +718,8 @@ __device__ __forceinline__ void copy4_scales(const Operand& A, const Operand& B,
 // last step reads stage 1 and scale buffer 1 only (K / 128 is a multiple of
 // 8), and every wave is past the step before it.  Its copies take the wait
 // states of lds_dma16_imm: between tiles the compiler reloads their offsets.
-template <int SM>
-__device__ __forceinline__ void prologue4(uint8_t* lds, const Operand& A, const Operand& B, int64_t K64, int wave,
+template <int SM, class OB = Operand>
+__device__ __forceinline__ void prologue4(uint8_t* lds, const Operand& A, const OB& B, int64_t K64, int wave,
                                           int a_blk, int b_blk) {
   const int K = (int)K64;
   const Copy4 co = copy4_offsets(K, wave, lane_id_fresh());
@@ -704,8 +738,8 @@ __device__ __forceinline__ void prologue4(uint8_t* lds, const Operand& A, const 
 // MXFP8 scales come in the layout of scale_blocks_kernel (a_blk / b_blk: the
 // byte offset of one scale block of A / B, rows x 16).  Step 0's copies were
 // issued by prologue4.
-template <int FA, int FB, int SM>
-__device__ __forceinline__ void mainloop4(uint8_t* lds, v4f (&acc)[8][8], const Operand& A, const Operand& B,
+template <int FA, int FB, int SM, bool WAIT = false, class OB = Operand>
+__device__ __forceinline__ void mainloop4(uint8_t* lds, v4f (&acc)[8][8], const Operand& A, const OB& B,
                                           int64_t K64, int wave, int a_blk = 0, int b_blk = 0) {
   static_assert(SM == SM_MX || SM == SM_PT, "E8M0 block scales or none");
   using LY = Big4;
@@ -746,10 +780,10 @@ __device__ __forceinline__ void mainloop4(uint8_t* lds, v4f (&acc)[8][8], const 
                "+v"(sb_off));
 
   auto copy = [&](int c, int kbase, uint32_t l_stage) __attribute__((always_inline)) {
-    copy4_data(A, B, co, c, K, kbase, l_stage, wave);
+    copy4_data<WAIT>(A, B, co, c, K, kbase, l_stage, wave);
   };
   auto copy_scales = [&](int blk, uint32_t l_sbuf, int k) __attribute__((always_inline)) {
-    copy4_scales(A, B, co, blk, l_sbuf, k, wave, a_blk, b_blk);
+    copy4_scales<WAIT>(A, B, co, blk, l_sbuf, k, wave, a_blk, b_blk);
   };
   int held[16];  // each fragment's scale dword of the current 4 steps (A 0..7, B 8..15)
   auto rd = [&](const uint8_t* stg, const uint8_t* sbuf, int off, int soff, int f, int sub, int h)

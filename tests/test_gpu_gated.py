@@ -272,3 +272,103 @@ def test_grouped_forward_and_backward(counts, behind):
             f.check(d[off:off + c])
         off += c
     assert (d[used:] == 0x55).all()
+
+
+# ---------------------------------------------------------------- every tile gives the same bits
+
+def quantized(seed, rows, k, fmt="e4m3", sigma=1.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    x = (torch.randn((rows, k), generator=g, device="cuda") * sigma).bfloat16()
+    q, s, _, _ = te().mxfp8_quantize(x, fmt, "row")
+    return q, s
+
+
+def run_forward(a, b, act, bias, out=None, workspace=None):
+    M, N = a[0].shape[0], b[0].shape[0] // 2
+    d = torch.full((M, N), 0x55, dtype=torch.uint8 if out else torch.int16, device="cuda")
+    ds = torch.full((M, N // 32), 0x55, dtype=torch.uint8, device="cuda") if out else None
+    aux = torch.full((M, 2 * N), 0x55, dtype=torch.int16, device="cuda")
+    te().te_mxfp8_gated_gemm(*a, "e4m3", *b, "e4m3", d, act, d_scale=ds, d_fmt=out, bias=bias, aux=aux,
+                             workspace=workspace)
+    return [t for t in (d, ds, aux) if t is not None]
+
+
+def run_backward(a, b, act, aux, workspace=None):
+    d = torch.full((a[0].shape[0], 2 * b[0].shape[0]), 0x55, dtype=torch.int16, device="cuda")
+    te().te_mxfp8_dgated_gemm(*a, "e4m3", *b, "e4m3", aux, d, act, workspace=workspace)
+    return [d]
+
+
+# (M, N, K) of grids that large tiles serve: ragged in both dimensions, an odd and an even number of K steps, one K
+# step; and K % 1024 == 0 grids with one and with several tiles per workgroup
+LARGE = [(1300, 4128, 384), (1300, 4128, 128), (1025, 5152, 256), (2100, 2336, 4096), (2100, 3744, 2048)]
+
+
+@pytest.mark.parametrize("M,N,K", LARGE)
+@pytest.mark.parametrize("out", [None, "e4m3", "e5m2"])
+def test_forward_large_grids_equal_their_rows_alone(M, N, K, out):
+    m = te()
+    a, b = quantized(1, M, K), quantized(2, 2 * N, K, sigma=0.05)
+    bias = torch.randn(2 * N, device="cuda").bfloat16()
+    act = "silu" if out else "gelu"
+    got = run_forward(a, b, act, bias, out)
+    size = m.te_mxfp8_gated_gemm_workspace_size(M, N, K)
+    if size:
+        ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+        again = run_forward(a, b, act, bias, out, ws)
+        assert all(torch.equal(x, y) for x, y in zip(got, again))
+    for r0 in (0, 448, M - 100):
+        rows = [t[r0:r0 + 100].clone() for t in a]
+        alone = run_forward(rows, b, act, bias, out)
+        assert all(torch.equal(x, y[r0:r0 + 100]) for x, y in zip(alone, got))
+
+
+def test_workspaces_serve_the_large_grids():
+    m = te()
+    assert m.te_mxfp8_gated_gemm_workspace_size(2100, 2336, 4096) > 0
+    assert m.te_mxfp8_gated_gemm_workspace_size(2100, 3744, 2048) > 0
+    assert m.te_mxfp8_gated_gemm_workspace_size(2100, 3744, 384) == 0
+    assert m.te_mxfp8_dgated_gemm_workspace_size(2100, 4656, 4096) > 0
+
+
+@pytest.mark.parametrize("M,N,K", [(1300, 8256, 384), (1300, 8256, 128), (2100, 4656, 4096), (2100, 7472, 2048)])
+def test_backward_large_grids_equal_their_rows_alone(M, N, K):
+    m = te()
+    a, b = quantized(3, M, K), quantized(4, N, K, sigma=0.05)
+    aux = torch.randn((M, 2 * N), device="cuda").bfloat16()
+    act = "silu" if K % 1024 else "gelu"
+    got, = run_backward(a, b, act, aux)
+    size = m.te_mxfp8_dgated_gemm_workspace_size(M, N, K)
+    if size:
+        ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+        assert torch.equal(run_backward(a, b, act, aux, ws)[0], got)
+    for r0 in (0, 448, M - 100):
+        alone, = run_backward([t[r0:r0 + 100].clone() for t in a], b, act, aux[r0:r0 + 100].clone())
+        assert torch.equal(alone, got[r0:r0 + 100])
+
+
+@pytest.mark.parametrize("counts", [[700, 0, 333, 515, 90], [2000, 1, 1]])
+def test_grouped_large_grids_equal_the_dense_call(counts):
+    m = te()
+    G, N, K, total = len(counts), 1040, 512, sum(counts)
+    a, b = quantized(5, total, K), quantized(6, G * 2 * N, K, sigma=0.05)
+    bias = torch.randn((G, 2 * N), device="cuda").bfloat16()
+    splits = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    d = torch.empty((total, N), dtype=torch.int16, device="cuda")
+    aux = torch.empty((total, 2 * N), dtype=torch.int16, device="cuda")
+    m.te_mxfp8_grouped_gated_gemm(splits, *a, "e4m3", *b, "e4m3", N, d, "silu", bias=bias, aux=aux)
+    pre = torch.randn((total, 2 * N), device="cuda").bfloat16()
+    dd = torch.empty((total, 2 * N), dtype=torch.int16, device="cuda")
+    m.te_mxfp8_grouped_dgated_gemm(splits, *a, "e4m3", *[t[:G * N] for t in b], "e4m3", N, pre, dd, "silu")
+    off = 0
+    for e, c in enumerate(counts):
+        if c >= 80:
+            rows = [t[off:off + c].clone() for t in a]
+            be = [t[e * 2 * N:(e + 1) * 2 * N].clone() for t in b]
+            want = run_forward(rows, be, "silu", bias[e].clone())
+            assert torch.equal(want[0], d[off:off + c]) and torch.equal(want[1], aux[off:off + c])
+            bb = [t[e * N:(e + 1) * N].clone() for t in b]
+            back, = run_backward(rows, bb, "silu", pre[off:off + c].clone())
+            assert torch.equal(back, dd[off:off + c])
+        off += c
