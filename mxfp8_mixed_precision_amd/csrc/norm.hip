@@ -9,6 +9,8 @@
 //
 // All statistics, products and sums are fp32; each output is rounded once.
 // The passes do ~10 operations per element: HBM bandwidth bounds them.
+#include <type_traits>
+
 #include "temx_device.h"
 
 namespace temx {
@@ -57,25 +59,71 @@ struct Vec16<4> {
   typedef u32x4 type __attribute__((aligned(4)));
 };
 
-// n: the chunk's valid elements (>= kChunk: all); elements past them read as 0
 template <class T>
-__device__ __forceinline__ Raw<T> load_chunk(const T* p, int n) {
+__device__ __forceinline__ Raw<T> load_whole(const T* p) {
   Raw<T> r;
-  constexpr int kV = sizeof(T) * kChunk / 16;
-  if (n >= kChunk) {
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      const u32x4 v = reinterpret_cast<const typename Vec16<sizeof(T)>::type*>(p)[i];
+  for (unsigned i = 0; i < sizeof(r.w) / 16; ++i) {
+    const u32x4 v = reinterpret_cast<const typename Vec16<sizeof(T)>::type*>(p)[i];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) r.w[4 * i + e] = v[e];
-    }
-  } else {
-    T t[kChunk];
-#pragma unroll
-    for (int e = 0; e < kChunk; ++e) t[e] = e < n ? p[e] : from_float<T>(0.f);
-    r = __builtin_bit_cast(Raw<T>, t);
+    for (int e = 0; e < 4; ++e) r.w[4 * i + e] = v[e];
   }
   return r;
+}
+
+// Element e becomes element e + k, and 0 past the chunk's end (0 <= k < kChunk).
+template <class T>
+__device__ __forceinline__ void shift_down(Raw<T>& r, int k) {
+  constexpr int kN = sizeof(r.w) / 4, kPer = 4 / sizeof(T);  // registers, elements of one
+#pragma unroll
+  for (int bit = kChunk / 2; bit >= kPer; bit >>= 1) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const uint32_t from = i + bit / kPer < kN ? r.w[i + bit / kPer] : 0u;
+      r.w[i] = (k & bit) ? from : r.w[i];
+    }
+  }
+  if constexpr (kPer == 2) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const uint32_t above = i + 1 < kN ? r.w[i + 1] : 0u;
+      r.w[i] = (k & 1) ? (r.w[i] >> 16 | above << 16) : r.w[i];
+    }
+  }
+}
+
+// Chunk at element c of a row of n elements (`row`); elements past the row read as 0.  The tail is the row's last
+// whole chunk's worth of elements, shifted: one access, and few registers.  Rows shorter than a chunk go element by
+// element.
+template <class T>
+__device__ __forceinline__ Raw<T> load_chunk(const T* row, int c, int n) {
+  if (n - c >= kChunk) return load_whole(row + c);
+  Raw<T> r;
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(r.w) / 4; ++i) r.w[i] = 0;
+  if (c < n && n >= kChunk) {
+    r = load_whole(row + n - kChunk);
+    shift_down<T>(r, c + kChunk - n);
+  } else if (c < n) {
+#pragma unroll 1
+    for (int e = n - 1; e >= 0; --e) {  // the elements so far one place up, and this one in front
+#pragma unroll
+      for (int i = sizeof(r.w) / 4 - 1; i >= 0; --i) {
+        const uint32_t below = i > 0 ? r.w[i - 1] : 0u;
+        r.w[i] = sizeof(T) == 4 ? below : (r.w[i] << 16 | below >> 16);
+      }
+      if constexpr (sizeof(T) == 4) r.w[0] = __builtin_bit_cast(uint32_t, row[e]);
+      else r.w[0] |= __builtin_bit_cast(uint16_t, row[e]);
+    }
+  }
+  return r;
+}
+
+// The chunk's registers as values the compiler knows nothing about.
+template <class T>
+__device__ __forceinline__ void opaque(Raw<T>& r) {
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(r.w) / 4; ++i) asm volatile("" : "+v"(r.w[i]));
 }
 
 template <class T>
@@ -123,15 +171,33 @@ __device__ __forceinline__ void store_chunk(T* p, const Raw<T>& r, int n) {
 }
 
 template <class T>
-__device__ __forceinline__ void load_floats(const T* p, int n, float (&f)[kChunk]) {
-  unpack<T>(load_chunk(p, n), f);
+__device__ __forceinline__ void load_floats(const T* row, int c, int n, float (&f)[kChunk]) {
+  unpack<T>(load_chunk(row, c, n), f);
 }
 
-// ---- block sums -------------------------------------------------------------
+// The thread's row among a workgroup's, NT threads each; the same for a whole wave (and known to be) from 64 up.
+template <int NT>
+__device__ __forceinline__ int row_lane() {
+  return NT >= 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / NT) : threadIdx.x / NT;
+}
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+// ---- sums across lanes -------------------------------------------------------
+
+// Sum over the LANES (16 or 64) lanes of a row group, in a fixed butterfly order: every lane ends with the same bits.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+  auto ror = [](float x, auto n) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x120 + decltype(n)::value, 0xF, 0xF, false));
+  };
+  v += ror(v, std::integral_constant<int, 8>{});  // row_ror within 16 lanes
+  v += ror(v, std::integral_constant<int, 4>{});
+  v += ror(v, std::integral_constant<int, 2>{});
+  v += ror(v, std::integral_constant<int, 1>{});
+  if constexpr (LANES == 64) {
+    const int lane = threadIdx.x & 63;
+    v += __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), 0x401F));                // lane ^ 16
+    v += __int_as_float(__builtin_amdgcn_ds_bpermute((lane ^ 32) << 2, __float_as_int(v)));  // lane ^ 32
+  }
   return v;
 }
 
@@ -139,7 +205,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 // again once every thread has returned from the next call or barrier.
 template <int THREADS>
 __device__ __forceinline__ float block_sum(float v, float* slots) {
-  v = wave_sum(v);
+  v = lanes_sum<64>(v);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
   __syncthreads();
@@ -147,6 +213,14 @@ __device__ __forceinline__ float block_sum(float v, float* slots) {
 #pragma unroll
   for (int w = 0; w < THREADS / 64; ++w) s += slots[w];
   return s;
+}
+
+// 1 / sqrt(v) to within one unit in the last place: the hardware's estimate and one Newton step, which is
+// left out where it has no value (v = 0 or infinite).
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const float r = rsqrtf(v);
+  const float e = __builtin_fmaf(-(v * r), r, 1.0f);
+  return __builtin_fabsf(e) < 0.5f ? __builtin_fmaf(0.5f * r, e, r) : r;
 }
 
 // ---- forward ----------------------------------------------------------------
@@ -184,6 +258,120 @@ __device__ __forceinline__ void store_mx(const Raw<bf16_t>& r, uint8_t* q, uint8
   }
 }
 
+// A row held in registers: NT threads per row, NC chunks per thread (thread t: chunks t, t + NT, ..), rows read
+// once.  The statistics of each wave's part are joined in one exchange: with n_w, m_w and M_w the count, mean and
+// centred sum of squares of wave w, mean = sum n_w m_w / n and M = sum M_w + n_w (m_w - mean)^2.
+template <class T, class W, int NT, int NC>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_fwd_kernel(NormFwd p) {
+  constexpr int kThreads = NT < 256 ? 256 : NT, kRows = kThreads / NT, kWaves = NT > 64 ? NT / 64 : 1;
+  constexpr int kLanes = NT < 64 ? NT : 64;
+  __shared__ float2 slots[kWaves];
+  const int n = p.cols, t = threadIdx.x % NT;
+  const int64_t row = (int64_t)blockIdx.x * kRows + row_lane<NT>(), at = row * n;
+  const bool row_ok = kRows == 1 || row < p.rows;  // every lane takes part in the exchanges below
+  float f[NC][kChunk];
+  Raw<T> raw[NC];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    const int c = (t + j * NT) * kChunk;
+    raw[j] = load_chunk(static_cast<const T*>(p.x) + at, c, row_ok ? n : 0);
+  }
+  if (p.residual != nullptr) {
+    Raw<T> res[NC];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int c = (t + j * NT) * kChunk;
+      res[j] = load_chunk(static_cast<const T*>(p.residual) + at, c, row_ok ? n : 0);
+    }
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int c = (t + j * NT) * kChunk;
+      float r[kChunk];
+      unpack<T>(raw[j], f[j]);
+      unpack<T>(res[j], r);
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) f[j][e] += r[e];
+      raw[j] = pack<T>(f[j]);
+      store_chunk(static_cast<T*>(p.sum) + at + c, raw[j], row_ok ? n - c : 0);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NC; ++j) unpack<T>(raw[j], f[j]);
+
+  // elements of the wave's lanes (of the row group's, NT < 64)
+  const int w0 = NT > 64 ? (t & ~63) * kChunk : 0;
+  auto held = [&](int first) {
+    int held = 0;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) held += min(max(n - first - j * NT * kChunk, 0), kLanes * kChunk);
+    return (float)held;
+  };
+  float mean = 0.f, m2 = 0.f;
+  if (p.layer) {
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) s += f[j][e];
+    s = lanes_sum<kLanes>(s);
+    const float cnt = held(w0);
+    mean = cnt > 0.f ? s / cnt : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    const int left = n - (t + j * NT) * kChunk;
+    if (left >= kChunk) {
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) m2 = __builtin_fmaf(f[j][e] - mean, f[j][e] - mean, m2);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e)
+        if (e < left) m2 = __builtin_fmaf(f[j][e] - mean, f[j][e] - mean, m2);
+    }
+  }
+  m2 = lanes_sum<kLanes>(m2);
+  if constexpr (NT > 64) {
+    if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = make_float2(mean, m2);
+    __syncthreads();
+    m2 = 0.f;
+    if (p.layer) {
+      mean = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) mean += slots[w].x * held(w * 64 * kChunk);
+      mean /= (float)n;
+    }
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float d = slots[w].x - mean;
+      m2 += slots[w].y;
+      if (p.layer) m2 = __builtin_fmaf(d * d, held(w * 64 * kChunk), m2);
+    }
+  }
+  const float rstd = inv_sqrt(m2 / (float)n + p.eps);
+
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    const int c = (t + j * NT) * kChunk, left = row_ok ? n - c : 0;
+    float g[kChunk];
+    load_floats(static_cast<const W*>(p.gamma), c, n, g);
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e) f[j][e] = ((f[j][e] - mean) * g[e]) * rstd;
+    if (p.beta != nullptr) {
+      load_floats(static_cast<const W*>(p.beta), c, n, g);
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) f[j][e] += g[e];
+    }
+    raw[j] = pack<T>(f[j]);
+    if (p.y != nullptr) store_chunk(static_cast<T*>(p.y) + at + c, raw[j], left);
+    if constexpr (__is_same(T, bf16_t))
+      if (p.q != nullptr) store_mx(raw[j], p.q, p.q_scale, at + c, left > 0, p.q_e5m2);
+  }
+  if (t == 0 && row_ok) {
+    if (p.mean != nullptr) p.mean[row] = mean;
+    if (p.rstd != nullptr) p.rstd[row] = rstd;
+  }
+}
+
 constexpr int kWideThreads = 1024;
 
 // One workgroup per row, the row read again for each of mean, variance and output: rows of any length.
@@ -198,10 +386,10 @@ __global__ __launch_bounds__(kWideThreads) void norm_fwd_wide_kernel(NormFwd p) 
     float s = 0.f;
     for (int c = threadIdx.x; c < nch; c += kWideThreads) {
       float f[kChunk];
-      load_floats(x + c * kChunk, n - c * kChunk, f);
+      load_floats(x, c * kChunk, n, f);
       if (p.residual) {
         float r[kChunk];
-        load_floats(static_cast<const T*>(p.residual) + at + c * kChunk, n - c * kChunk, r);
+        load_floats(static_cast<const T*>(p.residual) + at, c * kChunk, n, r);
 #pragma unroll
         for (int e = 0; e < kChunk; ++e) f[e] += r[e];
         const Raw<T> raw = pack<T>(f);
@@ -217,24 +405,24 @@ __global__ __launch_bounds__(kWideThreads) void norm_fwd_wide_kernel(NormFwd p) 
   float v = 0.f;
   for (int c = threadIdx.x; c < nch; c += kWideThreads) {
     float f[kChunk];
-    load_floats(x + c * kChunk, n - c * kChunk, f);
+    load_floats(x, c * kChunk, n, f);
 #pragma unroll
     for (int e = 0; e < kChunk; ++e)
       if (c * kChunk + e < n) v += (f[e] - mean) * (f[e] - mean);
   }
-  const float rstd = 1.0f / sqrtf(block_sum<kWideThreads>(v, slots) / (float)n + p.eps);
+  const float rstd = inv_sqrt(block_sum<kWideThreads>(v, slots) / (float)n + p.eps);
   // every lane of a wave takes part in the MXFP8 block maxima: the loop runs whole waves
   for (int c0 = 0; c0 < nch; c0 += kWideThreads) {
     const int c = c0 + threadIdx.x, left = n - c * kChunk;
     const bool ok = c < nch;
     float f[kChunk], g[kChunk], b[kChunk];
     if (ok) {
-      load_floats(x + c * kChunk, left, f);
-      load_floats(static_cast<const W*>(p.gamma) + c * kChunk, left, g);
+      load_floats(x, c * kChunk, n, f);
+      load_floats(static_cast<const W*>(p.gamma), c * kChunk, n, g);
 #pragma unroll
       for (int e = 0; e < kChunk; ++e) f[e] = (f[e] - mean) * rstd * g[e];
       if (p.beta) {
-        load_floats(static_cast<const W*>(p.beta) + c * kChunk, left, b);
+        load_floats(static_cast<const W*>(p.beta), c * kChunk, n, b);
 #pragma unroll
         for (int e = 0; e < kChunk; ++e) f[e] += b[e];
       }
@@ -271,6 +459,133 @@ struct NormBwd {
   int tiles;
 };
 
+// Rows held in registers as in norm_fwd_kernel; each workgroup walks rows and keeps its columns' sums of dy xh and
+// dy in registers, so dy and x are read once for dx and for the weights' gradients.  The next rows' loads are in
+// flight while a row is computed; xh and g are formed again after the row's sums (the row stays as it was loaded:
+// fewer registers, more workgroups).  At the end a workgroup's row lanes join in LDS and leave one row of partial
+// sums.
+template <class T, class W, int THREADS, int NT, int NC>
+__global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwd p) {
+  constexpr int kRows = THREADS / NT, kWaves = NT > 64 ? NT / 64 : 1, kLanes = NT < 64 ? NT : 64;
+  __shared__ float2 slots[2][THREADS / 64];
+  __shared__ float joined[kRows > 1 ? kRows - 1 : 1][kRows > 1 ? NT * kChunk : 1];
+  const int n = p.cols, t = threadIdx.x % NT, sub = row_lane<NT>();
+  const bool layer = p.mean != nullptr, skip = p.dskip != nullptr;
+  Raw<W> gamma[NC];
+  float dg[NC][kChunk], db[NC][kChunk];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    const int c = (t + j * NT) * kChunk;
+    gamma[j] = load_chunk(static_cast<const W*>(p.gamma), c, n);
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e) dg[j][e] = db[j][e] = 0.f;
+  }
+  struct Row {
+    Raw<T> x[NC], dy[NC], skip[NC];
+    float mean, rstd;
+  };
+  auto load = [&](Row& v, int64_t row) __attribute__((always_inline)) {
+    const bool ok = row < p.rows;  // a row past the end reads as zeros, with mean = rstd = 0
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int c = (t + j * NT) * kChunk;
+      const int64_t at = row * n;
+      v.x[j] = load_chunk(static_cast<const T*>(p.x) + at, c, ok ? n : 0);
+      v.dy[j] = load_chunk(static_cast<const T*>(p.dy) + at, c, ok ? n : 0);
+      if (skip) v.skip[j] = load_chunk(static_cast<const T*>(p.dskip) + at, c, ok ? n : 0);
+    }
+    v.mean = ok && layer ? p.mean[row] : 0.f;
+    v.rstd = ok ? p.rstd[row] : 0.f;
+  };
+  const float inv_n = 1.0f / (float)n;
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t base = (int64_t)blockIdx.x * kRows;
+  Row now, next;
+  load(now, base + sub);
+  int buf = 0;
+  for (; base < p.rows; base += step, buf ^= 1) {
+    if (base + step < p.rows) load(next, base + step + sub);  // in flight through this row
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      float xh[kChunk], d[kChunk], g[kChunk];
+      unpack<T>(now.x[j], xh);
+      unpack<T>(now.dy[j], d);
+      unpack<W>(gamma[j], g);
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) {
+        xh[e] = (xh[e] - now.mean) * now.rstd;
+        g[e] *= d[e];
+        s1 += g[e];
+        s2 = __builtin_fmaf(g[e], xh[e], s2);
+        dg[j][e] = __builtin_fmaf(d[e], xh[e], dg[j][e]);
+        db[j][e] += d[e];
+      }
+      __builtin_amdgcn_sched_barrier(0);  // chunk by chunk: interleaved they take more registers
+    }
+    s1 = lanes_sum<kLanes>(s1);
+    s2 = lanes_sum<kLanes>(s2);
+    if constexpr (NT > 64) {
+      // two buffers: a wave may be one row ahead of another, and the barrier of that row keeps it from two
+      if ((threadIdx.x & 63) == 0) slots[buf][threadIdx.x >> 6] = make_float2(s1, s2);
+      __syncthreads();
+      s1 = s2 = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        s1 += slots[buf][sub * kWaves + w].x;
+        s2 += slots[buf][sub * kWaves + w].y;
+      }
+    }
+    s1 = layer ? s1 * inv_n : 0.f;
+    s2 *= inv_n;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int c = (t + j * NT) * kChunk;
+      float xh[kChunk], d[kChunk], g[kChunk];
+      opaque(now.x[j]);  // formed again from here, not kept from above
+      opaque(now.dy[j]);
+      opaque(gamma[j]);
+      unpack<T>(now.x[j], xh);
+      unpack<T>(now.dy[j], d);
+      unpack<W>(gamma[j], g);
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e)
+        g[e] = now.rstd * (g[e] * d[e] - s1 - ((xh[e] - now.mean) * now.rstd) * s2);
+      if (skip) {
+        unpack<T>(now.skip[j], d);
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e) g[e] += d[e];
+      }
+      if (base + sub < p.rows) store_chunk(static_cast<T*>(p.dx) + (base + sub) * n + c, pack<T>(g), n - c);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    now = next;
+  }
+  // the row lanes' sums in order, one 8-column chunk per thread at a time
+  float* part = p.part + (int64_t)blockIdx.x * n;
+  for (int pass = 0; pass < (p.dbeta != nullptr ? 2 : 1); ++pass) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      float v[kChunk];
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) v[e] = pass ? db[j][e] : dg[j][e];
+      if constexpr (kRows > 1) {
+        __syncthreads();
+        if (sub > 0)
+#pragma unroll
+          for (int e = 0; e < kChunk; ++e) joined[sub - 1][e * NT + t] = v[e];
+        __syncthreads();
+        if (sub == 0)
+          for (int w = 0; w < kRows - 1; ++w)
+#pragma unroll
+            for (int e = 0; e < kChunk; ++e) v[e] += joined[w][e * NT + t];
+      }
+      const int c = (t + j * NT) * kChunk;
+      if (sub == 0) store_chunk(part + (int64_t)pass * p.tiles * n + c, pack<float>(v), n - c);
+    }
+  }
+}
+
 // dx, one workgroup per row, the row read twice: rows of any length.
 template <class T, class W>
 __global__ __launch_bounds__(kWideThreads) void norm_bwd_wide_kernel(NormBwd p) {
@@ -284,9 +599,9 @@ __global__ __launch_bounds__(kWideThreads) void norm_bwd_wide_kernel(NormBwd p) 
   for (int c = threadIdx.x; c < nch; c += kWideThreads) {
     float fx[kChunk], fd[kChunk], g[kChunk];
     const int left = n - c * kChunk;
-    load_floats(x + c * kChunk, left, fx);
-    load_floats(dy + c * kChunk, left, fd);
-    load_floats(static_cast<const W*>(p.gamma) + c * kChunk, left, g);
+    load_floats(x, c * kChunk, n, fx);
+    load_floats(dy, c * kChunk, n, fd);
+    load_floats(static_cast<const W*>(p.gamma), c * kChunk, n, g);
 #pragma unroll
     for (int e = 0; e < kChunk; ++e)
       if (e < left) {
@@ -300,13 +615,13 @@ __global__ __launch_bounds__(kWideThreads) void norm_bwd_wide_kernel(NormBwd p) 
   for (int c = threadIdx.x; c < nch; c += kWideThreads) {
     float fx[kChunk], fd[kChunk], g[kChunk];
     const int left = n - c * kChunk;
-    load_floats(x + c * kChunk, left, fx);
-    load_floats(dy + c * kChunk, left, fd);
-    load_floats(static_cast<const W*>(p.gamma) + c * kChunk, left, g);
+    load_floats(x, c * kChunk, n, fx);
+    load_floats(dy, c * kChunk, n, fd);
+    load_floats(static_cast<const W*>(p.gamma), c * kChunk, n, g);
 #pragma unroll
     for (int e = 0; e < kChunk; ++e) fx[e] = rstd * (fd[e] * g[e] - s1 - (fx[e] - mean) * rstd * s2);
     if (p.dskip) {
-      load_floats(static_cast<const T*>(p.dskip) + at + c * kChunk, left, g);
+      load_floats(static_cast<const T*>(p.dskip) + at, c * kChunk, n, g);
 #pragma unroll
       for (int e = 0; e < kChunk; ++e) fx[e] += g[e];
     }
@@ -331,8 +646,8 @@ __global__ __launch_bounds__(kColThreads) void norm_bwd_columns_kernel(NormBwd p
     for (int64_t r = r0 + ry; r < r1; r += kColLanes) {
       const float mean = p.mean ? p.mean[r] : 0.f, rstd = p.rstd[r];
       float fx[kChunk], fd[kChunk];
-      load_floats(static_cast<const T*>(p.x) + r * n + c * kChunk, left, fx);
-      load_floats(static_cast<const T*>(p.dy) + r * n + c * kChunk, left, fd);
+      load_floats(static_cast<const T*>(p.x) + r * n, c * kChunk, n, fx);
+      load_floats(static_cast<const T*>(p.dy) + r * n, c * kChunk, n, fd);
 #pragma unroll
       for (int e = 0; e < kChunk; ++e)
         if (e < left) {
@@ -364,8 +679,19 @@ __global__ __launch_bounds__(kFinCols* kFinLanes) void norm_bwd_final_kernel(Nor
   const int col = blockIdx.x * kFinCols + cx;
   const float* part = p.part + (int64_t)blockIdx.y * p.tiles * p.cols;
   float s = 0.f;
-  if (col < p.cols)
-    for (int t = ty; t < p.tiles; t += kFinLanes) s += part[(int64_t)t * p.cols + col];
+  if (col < p.cols) {
+    constexpr int kAhead = 8;  // loads in flight
+    for (int t0 = ty; t0 < p.tiles; t0 += kFinLanes * kAhead) {
+      float v[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int t = t0 + i * kFinLanes;
+        v[i] = t < p.tiles ? part[(int64_t)t * p.cols + col] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) s += v[i];
+    }
+  }
   red[ty][cx] = s;
   __syncthreads();
   if (ty == 0 && col < p.cols) {
@@ -376,28 +702,114 @@ __global__ __launch_bounds__(kFinCols* kFinLanes) void norm_bwd_final_kernel(Nor
   }
 }
 
-// Row tiles whose column sums are kept apart (one workspace row each per gradient).
+// Threads per row and chunks per thread of the register kernels; the longest row they take.
+struct NormShape {
+  int nt, nc;  // nt = 0: the wide kernels
+};
+constexpr int kMostFwd = 1024 * 4 * kChunk, kMostBwd = 1024 * kChunk;
+
+// Few rows take as many threads as a row has chunks (latency); many rows the fewest threads that hold the row.
+inline NormShape fwd_shape(int64_t rows, int64_t cols) {
+  const int64_t ch = (cols + kChunk - 1) / kChunk;
+  const bool few = rows <= device_cu_count();
+  if (ch <= 16) return {16, 1};
+  if (ch <= 64) return {64, 1};
+  if (ch <= 128 && !few) return {64, 2};
+  if (ch <= 256) return few ? NormShape{256, 1} : NormShape{64, 4};
+  if (ch <= 512 && !few) return {256, 2};
+  if (ch <= 1024) return few ? NormShape{1024, 1} : NormShape{256, 4};
+  if (ch <= 2048) return {1024, 2};
+  if (cols <= kMostFwd) return {1024, 4};
+  return {0, 0};
+}
+
+inline NormShape bwd_shape(int64_t cols) {
+  const int64_t ch = (cols + kChunk - 1) / kChunk;
+  if (ch <= 16) return {16, 1};
+  if (ch <= 64) return {64, 1};
+  if (ch <= 128) return {64, 2};
+  if (ch <= 256) return {256, 1};
+  if (ch <= 512) return {256, 2};
+  if (cols <= kMostBwd) return {1024, 1};
+  return {0, 0};
+}
+
+// Threads of a backward workgroup: 1024 where the registers allow it and it leaves a workgroup for every CU, else
+// 256 (or the row's).
+inline int bwd_threads(NormShape sh, int64_t rows) {
+  if (sh.nt == 1024) return 1024;
+  return sh.nc == 1 && rows * sh.nt >= (int64_t)device_cu_count() * 1024 ? 1024 : 256;
+}
+
+// Rows of partial sums of each weight gradient: the register kernel's workgroups, or the wide kernels' row tiles.
 inline int norm_tiles(int64_t rows, int64_t cols) {
-  (void)cols;
-  const int64_t t = (rows + 31) / 32;
-  return (int)(t < 256 ? t : 256);
+  const NormShape sh = bwd_shape(cols);
+  const int64_t cus = device_cu_count();
+  const int64_t per = sh.nt == 0 ? 32 : bwd_threads(sh, rows) / sh.nt;  // rows at a time
+  const int64_t most = sh.nt == 0 || bwd_threads(sh, rows) == 1024 ? cus : 2 * cus;
+  const int64_t t = (rows + per - 1) / per;
+  return (int)(t < most ? t : most);
 }
 
 bool float_dtype(te_dtype t) { return t == TE_BF16 || t == TE_FP16 || t == TE_FP32; }
 
 template <class T, class W>
 te_status run_fwd(const NormFwd& p, hipStream_t stream) {
-  hipLaunchKernelGGL((norm_fwd_wide_kernel<T, W>), dim3((unsigned)p.rows), dim3(kWideThreads), 0, stream, p);
+  const NormShape sh = fwd_shape(p.rows, p.cols);
+  auto go = [&](auto nt, auto nc) {
+    constexpr int NT = decltype(nt)::value, NC = decltype(nc)::value, kThreads = NT < 256 ? 256 : NT;
+    constexpr int kRows = kThreads / NT;
+    hipLaunchKernelGGL((norm_fwd_kernel<T, W, NT, NC>), dim3((unsigned)((p.rows + kRows - 1) / kRows)), dim3(kThreads),
+                       0, stream, p);
+  };
+  using std::integral_constant;
+  switch (sh.nt * 8 + sh.nc) {
+    case 16 * 8 + 1: go(integral_constant<int, 16>{}, integral_constant<int, 1>{}); break;
+    case 64 * 8 + 1: go(integral_constant<int, 64>{}, integral_constant<int, 1>{}); break;
+    case 64 * 8 + 2: go(integral_constant<int, 64>{}, integral_constant<int, 2>{}); break;
+    case 64 * 8 + 4: go(integral_constant<int, 64>{}, integral_constant<int, 4>{}); break;
+    case 256 * 8 + 1: go(integral_constant<int, 256>{}, integral_constant<int, 1>{}); break;
+    case 256 * 8 + 2: go(integral_constant<int, 256>{}, integral_constant<int, 2>{}); break;
+    case 256 * 8 + 4: go(integral_constant<int, 256>{}, integral_constant<int, 4>{}); break;
+    case 1024 * 8 + 1: go(integral_constant<int, 1024>{}, integral_constant<int, 1>{}); break;
+    case 1024 * 8 + 2: go(integral_constant<int, 1024>{}, integral_constant<int, 2>{}); break;
+    case 1024 * 8 + 4: go(integral_constant<int, 1024>{}, integral_constant<int, 4>{}); break;
+    default:
+      hipLaunchKernelGGL((norm_fwd_wide_kernel<T, W>), dim3((unsigned)p.rows), dim3(kWideThreads), 0, stream, p);
+  }
   return launch_status();
 }
 
 template <class T, class W>
 te_status run_bwd(const NormBwd& p, hipStream_t stream) {
+  const NormShape sh = bwd_shape(p.cols);
+  auto go = [&](auto nt, auto nc) {
+    constexpr int NT = decltype(nt)::value, NC = decltype(nc)::value, kSmall = NT < 256 ? 256 : NT;
+    if constexpr (NT <= 256 && NC == 1)
+      if (bwd_threads(sh, p.rows) == 1024) {
+        hipLaunchKernelGGL((norm_bwd_kernel<T, W, 1024, NT, NC>), dim3((unsigned)p.tiles), dim3(1024), 0, stream,
+                           p);
+        return;
+      }
+    hipLaunchKernelGGL((norm_bwd_kernel<T, W, kSmall, NT, NC>), dim3((unsigned)p.tiles), dim3(kSmall), 0,
+                       stream, p);
+  };
+  using std::integral_constant;
   if (p.rows > 0) {
-    hipLaunchKernelGGL((norm_bwd_wide_kernel<T, W>), dim3((unsigned)p.rows), dim3(kWideThreads), 0, stream, p);
-    hipLaunchKernelGGL((norm_bwd_columns_kernel<T>),
-                       dim3((unsigned)((p.cols + kColChunks * kChunk - 1) / (kColChunks * kChunk)), (unsigned)p.tiles),
-                       dim3(kColThreads), 0, stream, p);
+    switch (sh.nt * 8 + sh.nc) {
+      case 16 * 8 + 1: go(integral_constant<int, 16>{}, integral_constant<int, 1>{}); break;
+      case 64 * 8 + 1: go(integral_constant<int, 64>{}, integral_constant<int, 1>{}); break;
+      case 64 * 8 + 2: go(integral_constant<int, 64>{}, integral_constant<int, 2>{}); break;
+      case 256 * 8 + 1: go(integral_constant<int, 256>{}, integral_constant<int, 1>{}); break;
+      case 256 * 8 + 2: go(integral_constant<int, 256>{}, integral_constant<int, 2>{}); break;
+      case 1024 * 8 + 1: go(integral_constant<int, 1024>{}, integral_constant<int, 1>{}); break;
+      default:
+        hipLaunchKernelGGL((norm_bwd_wide_kernel<T, W>), dim3((unsigned)p.rows), dim3(kWideThreads), 0, stream, p);
+        hipLaunchKernelGGL((norm_bwd_columns_kernel<T>),
+                           dim3((unsigned)((p.cols + kColChunks * kChunk - 1) / (kColChunks * kChunk)),
+                                (unsigned)p.tiles),
+                           dim3(kColThreads), 0, stream, p);
+    }
   }
   hipLaunchKernelGGL((norm_bwd_final_kernel<W>),
                      dim3((unsigned)((p.cols + kFinCols - 1) / kFinCols), p.dbeta ? 2u : 1u),
