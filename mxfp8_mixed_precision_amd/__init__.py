@@ -409,86 +409,95 @@ def te_fp8_block_gemm(a, a_scale_inv, a_fmt, b, b_scale_inv, b_fmt, b_block_2d, 
 _NORM_DTYPES = {torch.bfloat16: TE_BF16, torch.float16: TE_FP16, torch.float32: TE_FP32}
 
 
-class _Call:
-    """One call of the entry points below: its tensors' checks, device and stream.  Every tensor has to be dense,
-    of the stated type and shape, and on the first one's device, which is the device the call runs on whatever the
-    current one is."""
+try:  # the current stream's handle without building a Stream object (2.8 us of a small call's 11)
+    from torch._C import _cuda_getCurrentRawStream as _current_stream
+except ImportError:
+    def _current_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
 
-    __slots__ = ("device",)
-
-    def __init__(self, first, name):
-        _require(isinstance(first, torch.Tensor), f"{name} is required")
-        self.device = first.device
-
-    def ptr(self, t, name, shape, dtypes, kind):
-        """Device address of a required tensor."""
-        if t is None:
-            raise ValueError(f"{name} is required")
-        if t.dtype not in dtypes:
-            raise ValueError(f"{name}: expected {kind}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, the first tensor on {self.device}")
-        return _ptr(t)
-
-    def opt(self, t, name, shape, dtypes, kind):
-        """Device address of an optional tensor (None stays None)."""
-        return None if t is None else self.ptr(t, name, shape, dtypes, kind)
-
-    def workspace(self, t):
-        """(address, bytes) of an optional workspace."""
-        if t is None:
-            return None, 0
-        if t.device != self.device:
-            raise ValueError(f"workspace is on {t.device}, the first tensor on {self.device}")
-        return _ptr(t), t.numel() * t.element_size()
-
-    def run(self, name, args, stream):
-        """The call with the tensors' device current, on `stream` or that device's current stream."""
-        if self.device.type != "cuda":
-            raise ValueError(f"expected a GPU tensor, got one on {self.device}")
-        if self.device.index == torch.cuda.current_device():
-            status = getattr(_lib, name)(*args, _stream(stream))
-        else:
-            with torch.cuda.device(self.device):
-                status = getattr(_lib, name)(*args, _stream(stream))
-        if status != TE_OK:
-            raise TemxError(name, status)
+_FLOATS = "bfloat16, float16 or float32"
+_CODES = "1-byte codes (uint8)"
+_B16 = "bf16 (or its int16 bits)"
+_KINDS = {_CODES: frozenset(_BYTE_DTYPES), _B16: frozenset(_BF16_DTYPES), "float32": (torch.float32,),
+          "int32": (torch.int32,), torch.bfloat16: (torch.bfloat16,), torch.float16: (torch.float16,),
+          torch.float32: (torch.float32,)}
 
 
-_FLOAT_KIND = "bfloat16, float16 or float32"
-_U8 = frozenset(_BYTE_DTYPES)
-_B16 = frozenset(_BF16_DTYPES)
-_F32 = frozenset((torch.float32,))
-_I32 = frozenset((torch.int32,))
+def _addr(t, name, shape, kind, index):
+    """Device address of a required tensor: dense, of this shape and kind, on the call's device (the index of the
+    first tensor's, -1 on the CPU)."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype not in _KINDS[kind]:
+        raise ValueError(f"{name}: expected {kind}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on the first tensor's device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor (row-major, no strides)")
+    return t.data_ptr()
+
+
+def _opt(t, name, shape, kind, index):
+    """Device address of an optional tensor (None stays None)."""
+    return None if t is None else _addr(t, name, shape, kind, index)
+
+
+def _workspace(t, index):
+    """(address, bytes) of an optional workspace."""
+    if t is None:
+        return None, 0
+    if t.get_device() != index:
+        raise ValueError(f"workspace is on {t.device}, not on the first tensor's device")
+    return _ptr(t), t.numel() * t.element_size()
+
+
+def _index_of(t, name):
+    _require(isinstance(t, torch.Tensor), f"{name} is required")
+    _require(t.dim() == 2, f"{name} must be 2-D")
+    return t.get_device()
+
+
+def _run(name, args, index, stream):
+    """The call with the tensors' device current, whatever the current one is, on `stream` or that device's current
+    stream."""
+    if index < 0:
+        raise ValueError("expected a GPU tensor, got one on the CPU")
+    handle = _current_stream(index) if stream is None else _stream(stream)
+    if index == torch.cuda.current_device():
+        status = getattr(_lib, name)(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = getattr(_lib, name)(*args, handle)
+    if status != TE_OK:
+        raise TemxError(name, status)
 
 
 def _norm_args(kind, x, gamma):
-    """(call, kind, rows, cols, x's dtype code and dtypes, gamma's dtype code and dtypes)"""
-    call = _Call(x, "x")
+    """(device index, kind, rows, cols, x's dtype code and dtype, gamma's dtype code and dtype)"""
+    index = _index_of(x, "x")
     k = NORM_KINDS[kind] if isinstance(kind, str) else int(kind)
-    _require(x.dim() == 2, "x must be 2-D")
-    rows, cols = x.shape
-    _require(x.dtype in _NORM_DTYPES, f"x: expected {_FLOAT_KIND}, got {x.dtype}")
-    _require(gamma is not None and (gamma.dtype == x.dtype or gamma.dtype == torch.float32),
+    xd = x.dtype
+    _require(xd in _NORM_DTYPES, f"x: expected {_FLOATS}, got {xd}")
+    _require(gamma is not None and (gamma.dtype == xd or gamma.dtype == torch.float32),
              "gamma: expected x's dtype or float32")
-    return call, k, rows, cols, _NORM_DTYPES[x.dtype], (x.dtype,), _NORM_DTYPES[gamma.dtype], (gamma.dtype,)
+    rows, cols = x.shape
+    return index, k, rows, cols, _NORM_DTYPES[xd], xd, _NORM_DTYPES[gamma.dtype], gamma.dtype
 
 
 def te_norm_forward(kind, x, gamma, beta=None, eps=1e-5, y=None, q=None, q_scale=None, q_fmt="e4m3", residual=None,
                     sum_out=None, mean=None, rstd=None, stream=None) -> None:
-    call, k, rows, cols, dt, xd, wdt, wd = _norm_args(kind, x, gamma)
+    i, k, rows, cols, dt, xd, wdt, wd = _norm_args(kind, x, gamma)
     full, w = (rows, cols), (cols,)
     if q is not None:
         _require(cols % 32 == 0, "q: the MXFP8 output needs cols % 32 == 0")
-    call.run("te_norm_forward", (
-        k, call.ptr(x, "x", full, xd, xd[0]), dt, rows, cols, call.opt(residual, "residual", full, xd, xd[0]),
-        call.ptr(gamma, "gamma", w, wd, wd[0]), call.opt(beta, "beta", w, wd, wd[0]), wdt, float(eps),
-        call.opt(sum_out, "sum_out", full, xd, xd[0]), call.opt(y, "y", full, xd, xd[0]),
-        call.opt(q, "q", full, _U8, "1-byte codes (uint8)"),
-        call.opt(q_scale, "q_scale", (rows, cols // 32), _U8, "1-byte codes (uint8)"), _fmt(q_fmt),
-        call.opt(mean, "mean", (rows,), _F32, "float32"), call.opt(rstd, "rstd", (rows,), _F32, "float32")), stream)
+    _run("te_norm_forward", (
+        k, _addr(x, "x", full, xd, i), dt, rows, cols, _opt(residual, "residual", full, xd, i),
+        _addr(gamma, "gamma", w, wd, i), _opt(beta, "beta", w, wd, i), wdt, eps, _opt(sum_out, "sum_out", full, xd, i),
+        _opt(y, "y", full, xd, i), _opt(q, "q", full, _CODES, i),
+        _opt(q_scale, "q_scale", (rows, cols // 32), _CODES, i), _fmt(q_fmt), _opt(mean, "mean", (rows,), "float32", i),
+        _opt(rstd, "rstd", (rows,), "float32", i)), i, stream)
 
 
 def te_norm_backward_workspace_size(rows: int, cols: int) -> int:
@@ -497,27 +506,25 @@ def te_norm_backward_workspace_size(rows: int, cols: int) -> int:
 
 def te_norm_backward(kind, dy, x, gamma, mean, rstd, dx, dgamma, dbeta=None, dskip=None, workspace=None,
                      stream=None) -> None:
-    call, k, rows, cols, dt, xd, wdt, wd = _norm_args(kind, x, gamma)
+    i, k, rows, cols, dt, xd, wdt, wd = _norm_args(kind, x, gamma)
     full, w = (rows, cols), (cols,)
-    ws, ws_bytes = call.workspace(workspace)
-    call.run("te_norm_backward", (
-        k, call.ptr(dy, "dy", full, xd, xd[0]), call.ptr(x, "x", full, xd, xd[0]),
-        call.opt(dskip, "dskip", full, xd, xd[0]), dt, rows, cols, call.ptr(gamma, "gamma", w, wd, wd[0]), wdt,
-        call.opt(mean, "mean", (rows,), _F32, "float32"), call.ptr(rstd, "rstd", (rows,), _F32, "float32"),
-        call.ptr(dx, "dx", full, xd, xd[0]), call.ptr(dgamma, "dgamma", w, wd, wd[0]),
-        call.opt(dbeta, "dbeta", w, wd, wd[0]), ws, ws_bytes), stream)
+    ws, ws_bytes = _workspace(workspace, i)
+    _run("te_norm_backward", (
+        k, _addr(dy, "dy", full, xd, i), _addr(x, "x", full, xd, i), _opt(dskip, "dskip", full, xd, i), dt, rows, cols,
+        _addr(gamma, "gamma", w, wd, i), wdt, _opt(mean, "mean", (rows,), "float32", i),
+        _addr(rstd, "rstd", (rows,), "float32", i), _addr(dx, "dx", full, xd, i), _addr(dgamma, "dgamma", w, wd, i),
+        _opt(dbeta, "dbeta", w, wd, i), ws, ws_bytes), i, stream)
 
 
 def _activation(act) -> int:
     return ACTIVATIONS[act] if isinstance(act, str) else int(act)
 
 
-def _gated_operands(call, a, a_scale, b, b_scale, rows_b):
+def _gated_operands(i, a, a_scale, b, b_scale, rows_b):
     """Addresses of a [M, K], a_scale, b [rows_b, K] and b_scale."""
     M, K = a.shape
-    kind = "1-byte codes (uint8)"
-    return (call.ptr(a, "a", (M, K), _U8, kind), call.ptr(a_scale, "a_scale", (M, K // 32), _U8, kind),
-            call.ptr(b, "b", (rows_b, K), _U8, kind), call.ptr(b_scale, "b_scale", (rows_b, K // 32), _U8, kind))
+    return (_addr(a, "a", (M, K), _CODES, i), _addr(a_scale, "a_scale", (M, K // 32), _CODES, i),
+            _addr(b, "b", (rows_b, K), _CODES, i), _addr(b_scale, "b_scale", (rows_b, K // 32), _CODES, i))
 
 
 def te_mxfp8_gated_gemm_workspace_size(M: int, N: int, K: int) -> int:
@@ -527,23 +534,22 @@ def te_mxfp8_gated_gemm_workspace_size(M: int, N: int, K: int) -> int:
 def te_mxfp8_gated_gemm(a, a_scale, a_fmt, b, b_scale, b_fmt, d, activation="silu", d_scale=None, d_fmt=None,
                         bias=None, aux=None, workspace=None, stream=None) -> None:
     """d_fmt None: d is bf16; "e4m3" / "e5m2": d is the MXFP8 operand (d, d_scale)."""
-    call = _Call(a, "a")
-    _require(a.dim() == 2 and b is not None and b.dim() == 2, "a and b must be 2-D")
+    i = _index_of(a, "a")
+    _require(b is not None and b.dim() == 2, "b must be 2-D")
     M, K = a.shape
     _require(b.shape[0] % 2 == 0, "b: expected an even number of rows (gate rows, then up rows)")
     N = b.shape[0] // 2
-    pa, psa, pb, psb = _gated_operands(call, a, a_scale, b, b_scale, 2 * N)
+    pa, psa, pb, psb = _gated_operands(i, a, a_scale, b, b_scale, 2 * N)
     if d_fmt is None:
-        pd, pds, out = call.ptr(d, "d", (M, N), _B16, "bf16 (or its int16 bits)"), None, TE_BF16
+        pd, pds, out = _addr(d, "d", (M, N), _B16, i), None, TE_BF16
         _require(d_scale is None, "d_scale: only with an MXFP8 d (d_fmt)")
     else:
-        pd, out = call.ptr(d, "d", (M, N), _U8, "1-byte codes (uint8)"), _fmt(d_fmt)
-        pds = call.ptr(d_scale, "d_scale", (M, N // 32), _U8, "1-byte codes (uint8)")
-    ws, ws_bytes = call.workspace(workspace)
-    call.run("te_mxfp8_gated_gemm", (
+        pd, out = _addr(d, "d", (M, N), _CODES, i), _fmt(d_fmt)
+        pds = _addr(d_scale, "d_scale", (M, N // 32), _CODES, i)
+    ws, ws_bytes = _workspace(workspace, i)
+    _run("te_mxfp8_gated_gemm", (
         pa, psa, _fmt(a_fmt), pb, psb, _fmt(b_fmt), M, N, K, _activation(activation), pd, pds, out,
-        call.opt(bias, "bias", (2 * N,), _B16, "bf16 (or its int16 bits)"),
-        call.opt(aux, "aux", (M, 2 * N), _B16, "bf16 (or its int16 bits)"), ws, ws_bytes), stream)
+        _opt(bias, "bias", (2 * N,), _B16, i), _opt(aux, "aux", (M, 2 * N), _B16, i), ws, ws_bytes), i, stream)
 
 
 def te_mxfp8_dgated_gemm_workspace_size(M: int, N: int, K: int) -> int:
@@ -552,45 +558,44 @@ def te_mxfp8_dgated_gemm_workspace_size(M: int, N: int, K: int) -> int:
 
 def te_mxfp8_dgated_gemm(a, a_scale, a_fmt, b, b_scale, b_fmt, aux, d, activation="silu", workspace=None,
                          stream=None) -> None:
-    call = _Call(a, "a")
-    _require(a.dim() == 2 and b is not None and b.dim() == 2, "a and b must be 2-D")
+    i = _index_of(a, "a")
+    _require(b is not None and b.dim() == 2, "b must be 2-D")
     M, K = a.shape
     N = b.shape[0]
-    pa, psa, pb, psb = _gated_operands(call, a, a_scale, b, b_scale, N)
-    ws, ws_bytes = call.workspace(workspace)
-    call.run("te_mxfp8_dgated_gemm", (
+    pa, psa, pb, psb = _gated_operands(i, a, a_scale, b, b_scale, N)
+    ws, ws_bytes = _workspace(workspace, i)
+    _run("te_mxfp8_dgated_gemm", (
         pa, psa, _fmt(a_fmt), pb, psb, _fmt(b_fmt), M, N, K, _activation(activation),
-        call.ptr(aux, "aux", (M, 2 * N), _B16, "bf16 (or its int16 bits)"),
-        call.ptr(d, "d", (M, 2 * N), _B16, "bf16 (or its int16 bits)"), ws, ws_bytes), stream)
+        _addr(aux, "aux", (M, 2 * N), _B16, i), _addr(d, "d", (M, 2 * N), _B16, i), ws, ws_bytes), i, stream)
+
+
+def _groups(m_splits, i):
+    """(count, address) of the splits."""
+    _require(m_splits is not None and m_splits.dim() == 1, "m_splits: expected a 1-D int32 tensor")
+    return m_splits.numel(), _addr(m_splits, "m_splits", m_splits.shape, "int32", i)
 
 
 def te_mxfp8_grouped_gated_gemm(m_splits, a, a_scale, a_fmt, b, b_scale, b_fmt, n: int, d, activation="silu",
                                 bias=None, aux=None, stream=None) -> None:
-    call = _Call(a, "a")
-    _require(m_splits is not None and m_splits.dim() == 1, "m_splits: expected a 1-D int32 tensor")
-    _require(a.dim() == 2, "a must be 2-D")
-    G, n = m_splits.numel(), int(n)
+    i, n = _index_of(a, "a"), int(n)
+    G, splits = _groups(m_splits, i)
     M, K = a.shape
-    pa, psa, pb, psb = _gated_operands(call, a, a_scale, b, b_scale, G * 2 * n)
-    call.run("te_mxfp8_grouped_gated_gemm", (
-        G, call.ptr(m_splits, "m_splits", (G,), _I32, "int32"), M, pa, psa, _fmt(a_fmt), pb, psb, _fmt(b_fmt), n, K,
-        _activation(activation), call.ptr(d, "d", (M, n), _B16, "bf16 (or its int16 bits)"),
-        call.opt(bias, "bias", (G, 2 * n), _B16, "bf16 (or its int16 bits)"),
-        call.opt(aux, "aux", (M, 2 * n), _B16, "bf16 (or its int16 bits)")), stream)
+    pa, psa, pb, psb = _gated_operands(i, a, a_scale, b, b_scale, G * 2 * n)
+    _run("te_mxfp8_grouped_gated_gemm", (
+        G, splits, M, pa, psa, _fmt(a_fmt), pb, psb, _fmt(b_fmt), n, K, _activation(activation),
+        _addr(d, "d", (M, n), _B16, i), _opt(bias, "bias", (G, 2 * n), _B16, i),
+        _opt(aux, "aux", (M, 2 * n), _B16, i)), i, stream)
 
 
 def te_mxfp8_grouped_dgated_gemm(m_splits, a, a_scale, a_fmt, b, b_scale, b_fmt, n: int, aux, d, activation="silu",
                                  stream=None) -> None:
-    call = _Call(a, "a")
-    _require(m_splits is not None and m_splits.dim() == 1, "m_splits: expected a 1-D int32 tensor")
-    _require(a.dim() == 2, "a must be 2-D")
-    G, n = m_splits.numel(), int(n)
+    i, n = _index_of(a, "a"), int(n)
+    G, splits = _groups(m_splits, i)
     M, K = a.shape
-    pa, psa, pb, psb = _gated_operands(call, a, a_scale, b, b_scale, G * n)
-    call.run("te_mxfp8_grouped_dgated_gemm", (
-        G, call.ptr(m_splits, "m_splits", (G,), _I32, "int32"), M, pa, psa, _fmt(a_fmt), pb, psb, _fmt(b_fmt), n, K,
-        _activation(activation), call.ptr(aux, "aux", (M, 2 * n), _B16, "bf16 (or its int16 bits)"),
-        call.ptr(d, "d", (M, 2 * n), _B16, "bf16 (or its int16 bits)")), stream)
+    pa, psa, pb, psb = _gated_operands(i, a, a_scale, b, b_scale, G * n)
+    _run("te_mxfp8_grouped_dgated_gemm", (
+        G, splits, M, pa, psa, _fmt(a_fmt), pb, psb, _fmt(b_fmt), n, K, _activation(activation),
+        _addr(aux, "aux", (M, 2 * n), _B16, i), _addr(d, "d", (M, 2 * n), _B16, i)), i, stream)
 
 
 # ------------------------------------------------------- allocating helpers
