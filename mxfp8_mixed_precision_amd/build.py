@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libtemx.so")
 SOURCES = ["quantize.hip", "amax_cast.hip", "gemm.hip", "block_gemm.hip", "block_gemm_e8m0.hip", "block_gemm_fp32.hip", "block_scale.hip",
            "block_quantize.hip", "norm.hip", "gated_gemm.hip",
-           "gated_gemm4.hip", "status.hip"]
+           "gated_gemm4.hip", "gated_rows.hip", "status.hip"]
 ARCH = "gfx950"
 
 

@@ -38,6 +38,10 @@ struct GatedParams {
 // The 4-wave tile's launch (gated_gemm4.hip), with the scales rearranged into the workspace.
 te_status launch_gated4(GatedParams p, bool backward, te_dtype fa, te_dtype fb, void* workspace, hipStream_t stream);
 
+// The launch for at most kFewRows rows (gated_rows.hip): forward, dense.
+constexpr int kFewRows = 64;
+te_status launch_gated_rows(const GatedParams& p, te_dtype fa, te_dtype fb, hipStream_t stream);
+
 namespace {
 
 // ---- activations ------------------------------------------------------------

@@ -49,6 +49,7 @@ template <bool BWD>
 te_status dense_gated(const GatedParams& p, te_dtype fa, te_dtype fb, void* workspace, size_t workspace_bytes,
                       hipStream_t stream) {
   const int64_t cols = BWD ? p.N : 2 * p.N;
+  if (!BWD && p.M <= kFewRows) return launch_gated_rows(p, fa, fb, stream);
   const size_t want = gated_workspace(p.M, cols, p.K, p.N);
   if (want > 0 && workspace != nullptr && workspace_bytes >= want && ((uintptr_t)workspace & 255u) == 0 &&
       aligned16(p.a_scale) && aligned16(p.b_scale))
