@@ -92,19 +92,19 @@ __device__ __forceinline__ void shift_down(Raw<T>& r, int k) {
   }
 }
 
-// Chunk at element c of a row of n elements (`row`); elements past the row read as 0.  The tail is the row's last
-// whole chunk's worth of elements, shifted: one access, and few registers.  Rows shorter than a chunk go element by
-// element.
+// Chunk at element c of a row of n elements, in two halves (zeros past the row).  load_ahead loads a tail lane's
+// chunk as the row's last kChunk elements, in the same instruction as every other lane's; settle, where the values
+// are first used, shifts a tail into place.  With the shift next to
+// the load a wave with a tail waited for each of its loads in turn (16384 x 1023 bf16 backward: 35 us that way).
+// Rows shorter than a chunk go element by element.
 template <class T>
-__device__ __forceinline__ Raw<T> load_chunk(const T* row, int c, int n) {
-  if (n - c >= kChunk) return load_whole(row + c);
+__device__ __forceinline__ Raw<T> load_ahead(const T* row, int c, int n) {
   Raw<T> r;
 #pragma unroll
   for (unsigned i = 0; i < sizeof(r.w) / 4; ++i) r.w[i] = 0;
-  if (c < n && n >= kChunk) {
-    r = load_whole(row + n - kChunk);
-    shift_down<T>(r, c + kChunk - n);
-  } else if (c < n) {
+  if (n >= kChunk) {
+    if (c < n) r = load_whole(row + min(c, n - kChunk));
+  } else if (c == 0) {
 #pragma unroll 1
     for (int e = n - 1; e >= 0; --e) {  // the elements so far one place up, and this one in front
 #pragma unroll
@@ -119,11 +119,17 @@ __device__ __forceinline__ Raw<T> load_chunk(const T* row, int c, int n) {
   return r;
 }
 
-// The chunk's registers as values the compiler knows nothing about.
 template <class T>
-__device__ __forceinline__ void opaque(Raw<T>& r) {
-#pragma unroll
-  for (unsigned i = 0; i < sizeof(r.w) / 4; ++i) asm volatile("" : "+v"(r.w[i]));
+__device__ __forceinline__ void settle(Raw<T>& r, int c, int n) {
+  const int k = c + kChunk - n;
+  if (n >= kChunk && k > 0 && k < kChunk) shift_down<T>(r, k);
+}
+
+template <class T>
+__device__ __forceinline__ Raw<T> load_chunk(const T* row, int c, int n) {
+  Raw<T> r = load_ahead(row, c, n);
+  settle<T>(r, c, n);
+  return r;
 }
 
 template <class T>
@@ -175,6 +181,9 @@ __device__ __forceinline__ void load_floats(const T* row, int c, int n, float (&
   unpack<T>(load_chunk(row, c, n), f);
 }
 
+// Rows that a workgroup of about `threads` threads holds, NT threads each.
+constexpr int rows_at_a_time(int nt, int threads) { return nt < threads ? threads / nt : 1; }
+
 // The thread's row among a workgroup's, NT threads each; the same for a whole wave (and known to be) from 64 up.
 template <int NT>
 __device__ __forceinline__ int row_lane() {
@@ -183,7 +192,7 @@ __device__ __forceinline__ int row_lane() {
 
 // ---- sums across lanes -------------------------------------------------------
 
-// Sum over the LANES (16 or 64) lanes of a row group, in a fixed butterfly order: every lane ends with the same bits.
+// Sum over the LANES (16, 32 or 64) lanes of a row group, in a fixed butterfly order: every lane ends with the same bits.
 template <int LANES>
 __device__ __forceinline__ float lanes_sum(float v) {
   auto ror = [](float x, auto n) {
@@ -193,9 +202,10 @@ __device__ __forceinline__ float lanes_sum(float v) {
   v += ror(v, std::integral_constant<int, 4>{});
   v += ror(v, std::integral_constant<int, 2>{});
   v += ror(v, std::integral_constant<int, 1>{});
+  if constexpr (LANES >= 32)
+    v += __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), 0x401F));  // lane ^ 16
   if constexpr (LANES == 64) {
     const int lane = threadIdx.x & 63;
-    v += __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), 0x401F));                // lane ^ 16
     v += __int_as_float(__builtin_amdgcn_ds_bpermute((lane ^ 32) << 2, __float_as_int(v)));  // lane ^ 32
   }
   return v;
@@ -262,31 +272,32 @@ __device__ __forceinline__ void store_mx(const Raw<bf16_t>& r, uint8_t* q, uint8
 // once.  The statistics of each wave's part are joined in one exchange: with n_w, m_w and M_w the count, mean and
 // centred sum of squares of wave w, mean = sum n_w m_w / n and M = sum M_w + n_w (m_w - mean)^2.
 template <class T, class W, int NT, int NC>
-__global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_fwd_kernel(NormFwd p) {
-  constexpr int kThreads = NT < 256 ? 256 : NT, kRows = kThreads / NT, kWaves = NT > 64 ? NT / 64 : 1;
+__global__ __launch_bounds__(NT* rows_at_a_time(NT, 256)) void norm_fwd_kernel(NormFwd p) {
+  constexpr int kRows = rows_at_a_time(NT, 256), kWaves = NT > 64 ? NT / 64 : 1;
   constexpr int kLanes = NT < 64 ? NT : 64;
-  __shared__ float2 slots[kWaves];
+  __shared__ float2 all_slots[kRows][kWaves];
+  float2(&slots)[kWaves] = all_slots[row_lane<NT>()];
   const int n = p.cols, t = threadIdx.x % NT;
   const int64_t row = (int64_t)blockIdx.x * kRows + row_lane<NT>(), at = row * n;
   const bool row_ok = kRows == 1 || row < p.rows;  // every lane takes part in the exchanges below
+  // A row past the end computes on the first and stores nothing.  sum_out may be one of the inputs: what a tail's or
+  // such a row's load may see changed is not used.
+  const int64_t from = row_ok ? at : 0;
   float f[NC][kChunk];
   Raw<T> raw[NC];
 #pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    const int c = (t + j * NT) * kChunk;
-    raw[j] = load_chunk(static_cast<const T*>(p.x) + at, c, row_ok ? n : 0);
-  }
+  for (int j = 0; j < NC; ++j) raw[j] = load_ahead(static_cast<const T*>(p.x) + from, (t + j * NT) * kChunk, n);
   if (p.residual != nullptr) {
     Raw<T> res[NC];
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      const int c = (t + j * NT) * kChunk;
-      res[j] = load_chunk(static_cast<const T*>(p.residual) + at, c, row_ok ? n : 0);
-    }
+    for (int j = 0; j < NC; ++j)
+      res[j] = load_ahead(static_cast<const T*>(p.residual) + from, (t + j * NT) * kChunk, n);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int c = (t + j * NT) * kChunk;
       float r[kChunk];
+      settle<T>(raw[j], c, n);
+      settle<T>(res[j], c, n);
       unpack<T>(raw[j], f[j]);
       unpack<T>(res[j], r);
 #pragma unroll
@@ -296,10 +307,13 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_fwd_kernel(NormFwd p
     }
   }
 #pragma unroll
-  for (int j = 0; j < NC; ++j) unpack<T>(raw[j], f[j]);
+  for (int j = 0; j < NC; ++j) {
+    if (p.residual == nullptr) settle<T>(raw[j], (t + j * NT) * kChunk, n);
+    unpack<T>(raw[j], f[j]);
+  }
 
   // elements of the wave's lanes (of the row group's, NT < 64)
-  const int w0 = NT > 64 ? (t & ~63) * kChunk : 0;
+  const int wave = NT > 64 ? __builtin_amdgcn_readfirstlane(t >> 6) : 0, w0 = wave * 64 * kChunk;
   auto held = [&](int first) {
     int held = 0;
 #pragma unroll
@@ -331,7 +345,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_fwd_kernel(NormFwd p
   }
   m2 = lanes_sum<kLanes>(m2);
   if constexpr (NT > 64) {
-    if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = make_float2(mean, m2);
+    if ((t & 63) == 0) slots[wave] = make_float2(mean, m2);
     __syncthreads();
     m2 = 0.f;
     if (p.layer) {
@@ -459,43 +473,33 @@ struct NormBwd {
   int tiles;
 };
 
-// Rows held in registers as in norm_fwd_kernel; each workgroup walks rows and keeps its columns' sums of dy xh and
+// Rows held in registers as in norm_fwd_kernel, a chunk per thread; each workgroup walks rows and keeps its columns' sums of dy xh and
 // dy in registers, so dy and x are read once for dx and for the weights' gradients.  The next rows' loads are in
-// flight while a row is computed; xh and g are formed again after the row's sums (the row stays as it was loaded:
-// fewer registers, more workgroups).  At the end a workgroup's row lanes join in LDS and leave one row of partial
-// sums.
-template <class T, class W, int THREADS, int NT, int NC>
-__global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwd p) {
-  constexpr int kRows = THREADS / NT, kWaves = NT > 64 ? NT / 64 : 1, kLanes = NT < 64 ? NT : 64;
-  __shared__ float2 slots[2][THREADS / 64];
+// flight while a row is computed.  At the end a workgroup's row lanes join in LDS and leave one row of partial sums.
+template <class T, class W, int THREADS, int NT>
+__global__ __launch_bounds__(NT* rows_at_a_time(NT, THREADS)) void norm_bwd_kernel(NormBwd p) {
+  constexpr int kRows = rows_at_a_time(NT, THREADS), kWaves = NT > 64 ? NT / 64 : 1, kLanes = NT < 64 ? NT : 64;
+  __shared__ float2 slots[2][kRows * kWaves];
   __shared__ float joined[kRows > 1 ? kRows - 1 : 1][kRows > 1 ? NT * kChunk : 1];
   const int n = p.cols, t = threadIdx.x % NT, sub = row_lane<NT>();
   const bool layer = p.mean != nullptr, skip = p.dskip != nullptr;
-  Raw<W> gamma[NC];
-  float dg[NC][kChunk], db[NC][kChunk];
+  const int c = t * kChunk;
+  Raw<W> gamma = load_chunk(static_cast<const W*>(p.gamma), c, n);
+  float dg[kChunk], db[kChunk];
 #pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    const int c = (t + j * NT) * kChunk;
-    gamma[j] = load_chunk(static_cast<const W*>(p.gamma), c, n);
-#pragma unroll
-    for (int e = 0; e < kChunk; ++e) dg[j][e] = db[j][e] = 0.f;
-  }
+  for (int e = 0; e < kChunk; ++e) dg[e] = db[e] = 0.f;
   struct Row {
-    Raw<T> x[NC], dy[NC], skip[NC];
+    Raw<T> x, dy, skip;
     float mean, rstd;
   };
   auto load = [&](Row& v, int64_t row) __attribute__((always_inline)) {
-    const bool ok = row < p.rows;  // a row past the end reads as zeros, with mean = rstd = 0
-#pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      const int c = (t + j * NT) * kChunk;
-      const int64_t at = row * n;
-      v.x[j] = load_chunk(static_cast<const T*>(p.x) + at, c, ok ? n : 0);
-      v.dy[j] = load_chunk(static_cast<const T*>(p.dy) + at, c, ok ? n : 0);
-      if (skip) v.skip[j] = load_chunk(static_cast<const T*>(p.dskip) + at, c, ok ? n : 0);
-    }
-    v.mean = ok && layer ? p.mean[row] : 0.f;
-    v.rstd = ok ? p.rstd[row] : 0.f;
+    row = min(row, p.rows - 1);  // a row past the end: the last one again, used for nothing
+    const int64_t at = row * n;
+    v.x = load_ahead(static_cast<const T*>(p.x) + at, c, n);
+    v.dy = load_ahead(static_cast<const T*>(p.dy) + at, c, n);
+    if (skip) v.skip = load_ahead(static_cast<const T*>(p.dskip) + at, c, n);
+    v.mean = layer ? p.mean[row] : 0.f;
+    v.rstd = p.rstd[row];
   };
   const float inv_n = 1.0f / (float)n;
   const int64_t step = (int64_t)gridDim.x * kRows;
@@ -506,28 +510,32 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwd p) {
   for (; base < p.rows; base += step, buf ^= 1) {
     if (base + step < p.rows) load(next, base + step + sub);  // in flight through this row
     float s1 = 0.f, s2 = 0.f;
+    const bool row_ok = base + sub < p.rows;
+    settle<T>(now.x, c, n);
+    settle<T>(now.dy, c, n);
+    float xh[kChunk], d[kChunk], g[kChunk];
+    unpack<T>(now.x, xh);
+    unpack<T>(now.dy, d);
+    unpack<W>(gamma, g);
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      float xh[kChunk], d[kChunk], g[kChunk];
-      unpack<T>(now.x[j], xh);
-      unpack<T>(now.dy[j], d);
-      unpack<W>(gamma[j], g);
+    for (int e = 0; e < kChunk; ++e) {
+      xh[e] = (xh[e] - now.mean) * now.rstd;
+      g[e] *= d[e];
+      s1 += g[e];
+      s2 = __builtin_fmaf(g[e], xh[e], s2);
+    }
+    if (row_ok) {
 #pragma unroll
       for (int e = 0; e < kChunk; ++e) {
-        xh[e] = (xh[e] - now.mean) * now.rstd;
-        g[e] *= d[e];
-        s1 += g[e];
-        s2 = __builtin_fmaf(g[e], xh[e], s2);
-        dg[j][e] = __builtin_fmaf(d[e], xh[e], dg[j][e]);
-        db[j][e] += d[e];
+        dg[e] = __builtin_fmaf(d[e], xh[e], dg[e]);
+        db[e] += d[e];
       }
-      __builtin_amdgcn_sched_barrier(0);  // chunk by chunk: interleaved they take more registers
     }
     s1 = lanes_sum<kLanes>(s1);
     s2 = lanes_sum<kLanes>(s2);
     if constexpr (NT > 64) {
       // two buffers: a wave may be one row ahead of another, and the barrier of that row keeps it from two
-      if ((threadIdx.x & 63) == 0) slots[buf][threadIdx.x >> 6] = make_float2(s1, s2);
+      if ((threadIdx.x & 63) == 0) slots[buf][threadIdx.x >> 6] = make_float2(s1, s2);  // NT % 64 == 0
       __syncthreads();
       s1 = s2 = 0.f;
 #pragma unroll
@@ -539,50 +547,34 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwd p) {
     s1 = layer ? s1 * inv_n : 0.f;
     s2 *= inv_n;
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      const int c = (t + j * NT) * kChunk;
-      float xh[kChunk], d[kChunk], g[kChunk];
-      opaque(now.x[j]);  // formed again from here, not kept from above
-      opaque(now.dy[j]);
-      opaque(gamma[j]);
-      unpack<T>(now.x[j], xh);
-      unpack<T>(now.dy[j], d);
-      unpack<W>(gamma[j], g);
+    for (int e = 0; e < kChunk; ++e) g[e] = now.rstd * (g[e] - s1 - xh[e] * s2);
+    if (skip) {
+      settle<T>(now.skip, c, n);
+      unpack<T>(now.skip, d);
 #pragma unroll
-      for (int e = 0; e < kChunk; ++e)
-        g[e] = now.rstd * (g[e] * d[e] - s1 - ((xh[e] - now.mean) * now.rstd) * s2);
-      if (skip) {
-        unpack<T>(now.skip[j], d);
-#pragma unroll
-        for (int e = 0; e < kChunk; ++e) g[e] += d[e];
-      }
-      if (base + sub < p.rows) store_chunk(static_cast<T*>(p.dx) + (base + sub) * n + c, pack<T>(g), n - c);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int e = 0; e < kChunk; ++e) g[e] += d[e];
     }
+    if (row_ok) store_chunk(static_cast<T*>(p.dx) + (base + sub) * n + c, pack<T>(g), n - c);
     now = next;
   }
   // the row lanes' sums in order, one 8-column chunk per thread at a time
   float* part = p.part + (int64_t)blockIdx.x * n;
   for (int pass = 0; pass < (p.dbeta != nullptr ? 2 : 1); ++pass) {
+    float v[kChunk];
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      float v[kChunk];
+    for (int e = 0; e < kChunk; ++e) v[e] = pass ? db[e] : dg[e];
+    if constexpr (kRows > 1) {
+      __syncthreads();
+      if (sub > 0)
 #pragma unroll
-      for (int e = 0; e < kChunk; ++e) v[e] = pass ? db[j][e] : dg[j][e];
-      if constexpr (kRows > 1) {
-        __syncthreads();
-        if (sub > 0)
+        for (int e = 0; e < kChunk; ++e) joined[sub - 1][e * NT + t] = v[e];
+      __syncthreads();
+      if (sub == 0)
+        for (int w = 0; w < kRows - 1; ++w)
 #pragma unroll
-          for (int e = 0; e < kChunk; ++e) joined[sub - 1][e * NT + t] = v[e];
-        __syncthreads();
-        if (sub == 0)
-          for (int w = 0; w < kRows - 1; ++w)
-#pragma unroll
-            for (int e = 0; e < kChunk; ++e) v[e] += joined[w][e * NT + t];
-      }
-      const int c = (t + j * NT) * kChunk;
-      if (sub == 0) store_chunk(part + (int64_t)pass * p.tiles * n + c, pack<float>(v), n - c);
+          for (int e = 0; e < kChunk; ++e) v[e] += joined[w][e * NT + t];
     }
+    if (sub == 0) store_chunk(part + (int64_t)pass * p.tiles * n + c, pack<float>(v), n - c);
   }
 }
 
@@ -702,113 +694,101 @@ __global__ __launch_bounds__(kFinCols* kFinLanes) void norm_bwd_final_kernel(Nor
   }
 }
 
-// Threads per row and chunks per thread of the register kernels; the longest row they take.
-struct NormShape {
-  int nt, nc;  // nt = 0: the wide kernels
-};
-constexpr int kMostFwd = 1024 * 4 * kChunk, kMostBwd = 1024 * kChunk;
-
-// Few rows take as many threads as a row has chunks (latency); many rows the fewest threads that hold the row.
-inline NormShape fwd_shape(int64_t rows, int64_t cols) {
+// Backward: threads per row (NT), one chunk per thread, rounded up to one of these; 0: the wide kernels.
+inline int bwd_threads_per_row(int64_t cols) {
   const int64_t ch = (cols + kChunk - 1) / kChunk;
-  const bool few = rows <= device_cu_count();
-  if (ch <= 16) return {16, 1};
-  if (ch <= 64) return {64, 1};
-  if (ch <= 128 && !few) return {64, 2};
-  if (ch <= 256) return few ? NormShape{256, 1} : NormShape{64, 4};
-  if (ch <= 512 && !few) return {256, 2};
-  if (ch <= 1024) return few ? NormShape{1024, 1} : NormShape{256, 4};
-  if (ch <= 2048) return {1024, 2};
-  if (cols <= kMostFwd) return {1024, 4};
-  return {0, 0};
+  for (int nt : {16, 32, 64, 128, 192, 256, 384, 512, 640, 768, 1024})
+    if (ch <= nt) return nt;
+  return 0;
 }
 
-inline NormShape bwd_shape(int64_t cols) {
-  const int64_t ch = (cols + kChunk - 1) / kChunk;
-  if (ch <= 16) return {16, 1};
-  if (ch <= 64) return {64, 1};
-  if (ch <= 128) return {64, 2};
-  if (ch <= 256) return {256, 1};
-  if (ch <= 512) return {256, 2};
-  if (cols <= kMostBwd) return {1024, 1};
-  return {0, 0};
-}
-
-// Threads of a backward workgroup: 1024 where the registers allow it and it leaves a workgroup for every CU, else
-// 256 (or the row's).
-inline int bwd_threads(NormShape sh, int64_t rows) {
-  if (sh.nt == 1024) return 1024;
-  return sh.nc == 1 && rows * sh.nt >= (int64_t)device_cu_count() * 1024 ? 1024 : 256;
+// Threads of a backward workgroup: 1024 where that leaves a workgroup for every CU, else 256 (or the row's).
+inline int bwd_threads(int nt, int64_t rows) {
+  return rows * nt >= (int64_t)device_cu_count() * 1024 ? 1024 : 256;
 }
 
 // Rows of partial sums of each weight gradient: the register kernel's workgroups, or the wide kernels' row tiles.
 inline int norm_tiles(int64_t rows, int64_t cols) {
-  const NormShape sh = bwd_shape(cols);
+  const int nt = bwd_threads_per_row(cols);
   const int64_t cus = device_cu_count();
-  const int64_t per = sh.nt == 0 ? 32 : bwd_threads(sh, rows) / sh.nt;  // rows at a time
-  const int64_t most = sh.nt == 0 || bwd_threads(sh, rows) == 1024 ? cus : 2 * cus;
+  const int64_t per = nt == 0 ? 32 : rows_at_a_time(nt, bwd_threads(nt, rows));  // rows at a time
+  const int64_t most = nt == 0 || nt * per > 640 ? cus : 2 * cus;
   const int64_t t = (rows + per - 1) / per;
   return (int)(t < most ? t : most);
 }
 
+// f(NT) for a row's threads, false where no register kernel takes the row
+template <class F>
+bool with_threads(int nt, F f) {
+  switch (nt) {
+    case 16: f(std::integral_constant<int, 16>{}); return true;
+    case 32: f(std::integral_constant<int, 32>{}); return true;
+    case 64: f(std::integral_constant<int, 64>{}); return true;
+    case 128: f(std::integral_constant<int, 128>{}); return true;
+    case 192: f(std::integral_constant<int, 192>{}); return true;
+    case 256: f(std::integral_constant<int, 256>{}); return true;
+    case 384: f(std::integral_constant<int, 384>{}); return true;
+    case 512: f(std::integral_constant<int, 512>{}); return true;
+    case 640: f(std::integral_constant<int, 640>{}); return true;
+    case 768: f(std::integral_constant<int, 768>{}); return true;
+    case 1024: f(std::integral_constant<int, 1024>{}); return true;
+    default: return false;
+  }
+}
+
 bool float_dtype(te_dtype t) { return t == TE_BF16 || t == TE_FP16 || t == TE_FP32; }
 
+// Forward: a wave (or less) per row up to 256 chunks and 256 threads up to 1024, up to 4 chunks per thread: several
+// rows' loads are in flight per CU and few waves have to meet (8192 x 8192 bf16: 52 us with 256 x 4, 76 with
+// 1024 x 1; 8192 x 4096: 29 and 35).  At most a row per CU takes a thread per chunk instead (1 x 8192: 3.8 us).
 template <class T, class W>
 te_status run_fwd(const NormFwd& p, hipStream_t stream) {
-  const NormShape sh = fwd_shape(p.rows, p.cols);
   auto go = [&](auto nt, auto nc) {
-    constexpr int NT = decltype(nt)::value, NC = decltype(nc)::value, kThreads = NT < 256 ? 256 : NT;
-    constexpr int kRows = kThreads / NT;
-    hipLaunchKernelGGL((norm_fwd_kernel<T, W, NT, NC>), dim3((unsigned)((p.rows + kRows - 1) / kRows)), dim3(kThreads),
-                       0, stream, p);
+    constexpr int NT = decltype(nt)::value, NC = decltype(nc)::value, kRows = rows_at_a_time(NT, 256);
+    hipLaunchKernelGGL((norm_fwd_kernel<T, W, NT, NC>), dim3((unsigned)((p.rows + kRows - 1) / kRows)),
+                       dim3(NT * kRows), 0, stream, p);
   };
   using std::integral_constant;
-  switch (sh.nt * 8 + sh.nc) {
-    case 16 * 8 + 1: go(integral_constant<int, 16>{}, integral_constant<int, 1>{}); break;
-    case 64 * 8 + 1: go(integral_constant<int, 64>{}, integral_constant<int, 1>{}); break;
-    case 64 * 8 + 2: go(integral_constant<int, 64>{}, integral_constant<int, 2>{}); break;
-    case 64 * 8 + 4: go(integral_constant<int, 64>{}, integral_constant<int, 4>{}); break;
-    case 256 * 8 + 1: go(integral_constant<int, 256>{}, integral_constant<int, 1>{}); break;
-    case 256 * 8 + 2: go(integral_constant<int, 256>{}, integral_constant<int, 2>{}); break;
-    case 256 * 8 + 4: go(integral_constant<int, 256>{}, integral_constant<int, 4>{}); break;
-    case 1024 * 8 + 1: go(integral_constant<int, 1024>{}, integral_constant<int, 1>{}); break;
-    case 1024 * 8 + 2: go(integral_constant<int, 1024>{}, integral_constant<int, 2>{}); break;
-    case 1024 * 8 + 4: go(integral_constant<int, 1024>{}, integral_constant<int, 4>{}); break;
-    default:
-      hipLaunchKernelGGL((norm_fwd_wide_kernel<T, W>), dim3((unsigned)p.rows), dim3(kWideThreads), 0, stream, p);
-  }
+  const int ch = (int)(((int64_t)p.cols + kChunk - 1) / kChunk);
+  const bool few = p.rows <= device_cu_count();
+  if (ch <= 16) go(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  else if (ch <= 32) go(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  else if (ch <= 64) go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  else if (ch <= 256 && few) go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+  else if (ch <= 128) go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  else if (ch <= 192) go(integral_constant<int, 64>{}, integral_constant<int, 3>{});
+  else if (ch <= 256) go(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+  else if (ch <= 1024 && few) go(integral_constant<int, 1024>{}, integral_constant<int, 1>{});
+  else if (ch <= 512) go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  else if (ch <= 768) go(integral_constant<int, 256>{}, integral_constant<int, 3>{});
+  else if (ch <= 1024) go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  else if (ch <= 2048) go(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+  else if (ch <= 4096) go(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
+  else hipLaunchKernelGGL((norm_fwd_wide_kernel<T, W>), dim3((unsigned)p.rows), dim3(kWideThreads), 0, stream, p);
   return launch_status();
 }
 
 template <class T, class W>
 te_status run_bwd(const NormBwd& p, hipStream_t stream) {
-  const NormShape sh = bwd_shape(p.cols);
-  auto go = [&](auto nt, auto nc) {
-    constexpr int NT = decltype(nt)::value, NC = decltype(nc)::value, kSmall = NT < 256 ? 256 : NT;
-    if constexpr (NT <= 256 && NC == 1)
-      if (bwd_threads(sh, p.rows) == 1024) {
-        hipLaunchKernelGGL((norm_bwd_kernel<T, W, 1024, NT, NC>), dim3((unsigned)p.tiles), dim3(1024), 0, stream,
-                           p);
-        return;
-      }
-    hipLaunchKernelGGL((norm_bwd_kernel<T, W, kSmall, NT, NC>), dim3((unsigned)p.tiles), dim3(kSmall), 0,
-                       stream, p);
-  };
-  using std::integral_constant;
+  const dim3 tiles((unsigned)p.tiles);
   if (p.rows > 0) {
-    switch (sh.nt * 8 + sh.nc) {
-      case 16 * 8 + 1: go(integral_constant<int, 16>{}, integral_constant<int, 1>{}); break;
-      case 64 * 8 + 1: go(integral_constant<int, 64>{}, integral_constant<int, 1>{}); break;
-      case 64 * 8 + 2: go(integral_constant<int, 64>{}, integral_constant<int, 2>{}); break;
-      case 256 * 8 + 1: go(integral_constant<int, 256>{}, integral_constant<int, 1>{}); break;
-      case 256 * 8 + 2: go(integral_constant<int, 256>{}, integral_constant<int, 2>{}); break;
-      case 1024 * 8 + 1: go(integral_constant<int, 1024>{}, integral_constant<int, 1>{}); break;
-      default:
-        hipLaunchKernelGGL((norm_bwd_wide_kernel<T, W>), dim3((unsigned)p.rows), dim3(kWideThreads), 0, stream, p);
-        hipLaunchKernelGGL((norm_bwd_columns_kernel<T>),
-                           dim3((unsigned)((p.cols + kColChunks * kChunk - 1) / (kColChunks * kChunk)),
-                                (unsigned)p.tiles),
-                           dim3(kColThreads), 0, stream, p);
+    const int nt = bwd_threads_per_row(p.cols);
+    const bool held = with_threads(nt, [&](auto n) {
+      constexpr int NT = decltype(n)::value;
+      if constexpr (rows_at_a_time(NT, 1024) > 1)
+        if (bwd_threads(nt, p.rows) == 1024) {
+          hipLaunchKernelGGL((norm_bwd_kernel<T, W, 1024, NT>), tiles, dim3(NT * rows_at_a_time(NT, 1024)), 0, stream,
+                             p);
+          return;
+        }
+      hipLaunchKernelGGL((norm_bwd_kernel<T, W, 256, NT>), tiles, dim3(NT * rows_at_a_time(NT, 256)), 0, stream, p);
+    });
+    if (!held) {
+      hipLaunchKernelGGL((norm_bwd_wide_kernel<T, W>), dim3((unsigned)p.rows), dim3(kWideThreads), 0, stream, p);
+      hipLaunchKernelGGL((norm_bwd_columns_kernel<T>),
+                         dim3((unsigned)((p.cols + kColChunks * kChunk - 1) / (kColChunks * kChunk)),
+                              (unsigned)p.tiles),
+                         dim3(kColThreads), 0, stream, p);
     }
   }
   hipLaunchKernelGGL((norm_bwd_final_kernel<W>),
