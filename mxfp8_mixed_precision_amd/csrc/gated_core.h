@@ -51,29 +51,30 @@ __device__ __forceinline__ float silu(float x) {
   return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * x));
 }
 
-// silu and its derivative s + x s (1 - s), s = 1 / (1 + e); s (1 - s) = 1 / (2 + e + 1 / e) keeps its relative
-// accuracy in both tails, and the product is 0 once that factor is (x may be infinite there)
-__device__ __forceinline__ void silu_and_grad(float x, float& v, float& dv) {
-  const float e = __builtin_amdgcn_exp2f(-1.4426950408889634f * x);
-  const float s = __builtin_amdgcn_rcpf(1.0f + e);
-  const float sd = __builtin_amdgcn_rcpf(2.0f + e + __builtin_amdgcn_rcpf(e));
-  v = x * s;
-  dv = s + (sd == 0.0f ? 0.0f : x * sd);
-}
-
 template <int ACT>
 __device__ __forceinline__ float act_value(float x) {
   if constexpr (ACT == TE_ACT_SILU) return silu(x);
   else return gelu_tanh(x);
 }
 
+// act(x) = x s and its derivative s + x s (1 - s) w with s = 1 / (1 + e): silu has e = 2^(-x log2 e) and w = 1; GELU
+// e = 2^(-2 u log2 e) (u as in gelu_tanh) and w = 2 du/dx.  The product s (1 - s) x w takes x within +-128, where s
+// has long been 0 or 1: far gates then give 0 or 1 and never 0 times infinity.  1 - s is rounded to 2^-25 at worst,
+// which s (>= 1/2 there) dwarfs.  Two transcendentals in all: one wave per SIMD computes the 4-wave tile's epilogue,
+// which took 29 us a tile with the four of dgelu_tanh and is bound by neither its loads nor its stores.
 template <int ACT>
 __device__ __forceinline__ void act_and_grad(float x, float& v, float& dv) {
+  const float c = __builtin_amdgcn_fmed3f(x, -128.0f, 128.0f);
   if constexpr (ACT == TE_ACT_SILU) {
-    silu_and_grad(x, v, dv);
+    const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * x));
+    v = x * s;
+    dv = __builtin_fmaf(c * s, 1.0f - s, s);
   } else {
-    v = gelu_tanh(x);
-    dv = dgelu_tanh(x);
+    constexpr float kK = 0.7978845608028654f;                       // sqrt(2/pi)
+    constexpr float kC = -2.0f * kK * 1.4426950408889634f;          // -2 sqrt(2/pi) log2(e)
+    const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * (kC + (kC * 0.044715f) * (x * x))));
+    v = x * s;
+    dv = __builtin_fmaf(c * s * (1.0f - s), 2.0f * kK + (6.0f * kK * 0.044715f) * (c * c), s);
   }
 }
 
@@ -184,6 +185,7 @@ __device__ __forceinline__ GatedOperand4 make_gated_operand4(const uint8_t* b, c
 // bytes of each of 16 rows.  A region is 16 KB; LDS accesses of one wave
 // complete in order, so a region needs no barrier of its own.
 constexpr int kRegion = 16 * 1024;
+constexpr int kNonTemporal = 2;  // cache policy of a buffer access
 constexpr int kOutOfRange = (int)0x80000000u;  // a buffer offset past every tile's rows (at most 2^31 bytes)
 
 __device__ __forceinline__ void bf16x4(uint2 v, float (&f)[4]) {
@@ -233,6 +235,14 @@ __device__ __forceinline__ RowBuffer row_buffer(const void* t, int64_t stride, i
   return r;
 }
 
+// 16 bytes to row `row` of a buffer.  The row goes into the lane's offset and not into the scalar one: with a scalar
+// offset the compiler takes a wide store's data registers as free for the next VALU instruction, and on gfx950 such a
+// write has reached the stored data (first dword, every other 8 lanes).
+template <int POLICY>
+__device__ __forceinline__ void store16(const RowBuffer& to, u32x4 v, int row) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, to.rsrc, to.off + row * to.stride, 0, POLICY);
+}
+
 template <int CH>
 __device__ __forceinline__ int region_off(int t, int lane) {
   const int q = (64 * t + lane) / CH, c = lane % CH;
@@ -240,12 +250,12 @@ __device__ __forceinline__ int region_off(int t, int lane) {
 }
 
 // ROWS rows x CH chunks of a region to the buffer's rows row0 ..
-template <int CH, int ROWS>
+template <int CH, int ROWS, int POLICY = 0>
 __device__ __forceinline__ void store_rows(const uint8_t* region, const RowBuffer& to, int row0, int lane) {
 #pragma unroll
   for (int t = 0; t < ROWS * CH / 64; ++t) {
     const u32x4 v = *reinterpret_cast<const u32x4*>(region + region_off<CH>(t, lane));
-    __builtin_amdgcn_raw_buffer_store_b128(v, to.rsrc, to.off, (row0 + t * (64 / CH)) * to.stride, 0);
+    store16<POLICY>(to, v, row0 + t * (64 / CH));
   }
 }
 
@@ -360,73 +370,75 @@ __device__ __forceinline__ void epilogue_gated(v4f (&acc)[LY::FRN][LY::FRM], uin
   }
 }
 
-// Backward: fragment i holds columns n0 + WTN wn + 16 i + 4 g + e of acc; blocks of rows of aux come through the
-// region the same way the gradients leave (row = gate chunks, then up chunks).
+// Backward: fragment i holds columns n0 + WTN wn + 16 i + 4 g + e of acc.  Blocks of 16 rows of aux come through
+// the wave's region the same way the gradients leave (row = gate chunks, then up chunks), a block's loads in flight
+// while the one before is computed, the first's from before the epilogue (begin).
 template <class LY>
-__device__ __forceinline__ void epilogue_dgated(v4f (&acc)[LY::FRN][LY::FRM], uint8_t* lds, const GatedParams& p,
-                                                int64_t m0, int64_t m_end, int64_t n0, int wave, int lane) {
-  constexpr int CH = LY::WTN / 4, FRH = 1, ROWS = 16 * FRH;
-  constexpr int kT = ROWS * CH / 64;  // 16-byte accesses per lane and block
+struct DgatedAux {
+  static constexpr int CH = LY::WTN / 4, ROWS = 16, kT = ROWS * CH / 64;  // 16-byte accesses per lane and block
+  static constexpr int kPolicy = in_agprs<LY>() ? kNonTemporal : 0;
   static_assert((CH & (CH - 1)) == 0, "staging layout");
-  const int wm = wave / LY::NWN, wn = wave % LY::NWN;
-  const int g = lane >> 4, r = lane & 15;
-  const int64_t N = p.N, mw = m0 + wm * LY::WTM, nw = n0 + wn * LY::WTN;
-  uint8_t* region = lds + wave * (ROWS * CH * 16);
-  const RowBuffer from = row_buffer<CH, 16, true>(p.aux, 4 * N, 2 * N, mw, m_end, LY::WTM, nw, N, lane);
-  const RowBuffer to = row_buffer<CH, 16, true>(p.d, 4 * N, 2 * N, mw, m_end, LY::WTM, nw, N, lane);
+  RowBuffer from;
   u32x4 v[kT];
-  auto load = [&](int h) __attribute__((always_inline)) {
+
+  __device__ __forceinline__ void load(int h) {
 #pragma unroll
     for (int t = 0; t < kT; ++t)
-      v[t] = __builtin_amdgcn_raw_buffer_load_b128(from.rsrc, from.off, (ROWS * h + t * (64 / CH)) * from.stride, 0);
-  };
-  load(0);
+      v[t] = __builtin_amdgcn_raw_buffer_load_b128(from.rsrc, from.off, (ROWS * h + t * (64 / CH)) * from.stride,
+                                                   kPolicy);
+  }
+  __device__ __forceinline__ void begin(const GatedParams& p, int64_t m0, int64_t m_end, int64_t n0, int wave,
+                                        int lane) {
+    const int64_t mw = m0 + wave / LY::NWN * LY::WTM, nw = n0 + wave % LY::NWN * LY::WTN;
+    from = row_buffer<CH, 16, true>(p.aux, 4 * p.N, 2 * p.N, mw, m_end, LY::WTM, nw, p.N, lane);
+    load(0);
+  }
+};
+
+template <class LY>
+__device__ __forceinline__ void epilogue_dgated(v4f (&acc)[LY::FRN][LY::FRM], uint8_t* lds, const GatedParams& p,
+                                                DgatedAux<LY>& aux, int64_t m0, int64_t m_end, int64_t n0, int wave,
+                                                int lane) {
+  using X = DgatedAux<LY>;
+  constexpr int CH = X::CH;
+  const int g = lane >> 4, r = lane & 15;
+  const int64_t N = p.N, mw = m0 + wave / LY::NWN * LY::WTM, nw = n0 + wave % LY::NWN * LY::WTN;
+  uint8_t* region = lds + wave * (X::ROWS * CH * 16);
+  const RowBuffer to = row_buffer<CH, 16, true>(p.d, 4 * N, 2 * N, mw, m_end, LY::WTM, nw, N, lane);
   __syncthreads();  // every wave's reads of the last stage are done: the LDS is free
 #pragma unroll
-  for (int h = 0; h < LY::FRM / FRH; ++h) {
+  for (int h = 0; h < LY::FRM; ++h) {
 #pragma unroll
-    for (int t = 0; t < kT; ++t) *reinterpret_cast<u32x4*>(region + region_off<CH>(t, lane)) = v[t];
-    if (h + 1 < LY::FRM / FRH) load(h + 1);  // in flight while this block is computed
+    for (int t = 0; t < X::kT; ++t) *reinterpret_cast<u32x4*>(region + region_off<CH>(t, lane)) = aux.v[t];
+    if (h + 1 < LY::FRM) aux.load(h + 1);
     asm volatile("" ::: "memory");
     auto gradients = [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
-      for (int jj = 0; jj < FRH; ++jj)
+      for (int i = 0; i < LY::FRN; ++i) {
+        if constexpr (in_agprs<LY>()) asm volatile("" : "+a"(acc[i][h]));
+        uint2* pg = reinterpret_cast<uint2*>(region + frag_off<CH>(0, i, g, r));
+        uint2* pu = reinterpret_cast<uint2*>(region + frag_off<CH>(0, LY::FRN + i, g, r));
+        float ga[4], up[4];
+        bf16x4(*pg, ga);
+        bf16x4(*pu, up);
 #pragma unroll
-        for (int i = 0; i < LY::FRN; ++i) {
-          const int j = FRH * h + jj;
-          if constexpr (in_agprs<LY>()) asm volatile("" : "+a"(acc[i][j]));
-          uint2* pg = reinterpret_cast<uint2*>(region + frag_off<CH>(jj, i, g, r));
-          uint2* pu = reinterpret_cast<uint2*>(region + frag_off<CH>(jj, LY::FRN + i, g, r));
-          float ga[4], up[4];
-          bf16x4(*pg, ga);
-          bf16x4(*pu, up);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float a = acc[i][j][e];
-            float f, df;
-            act_and_grad<decltype(act)::value>(ga[e], f, df);
-            ga[e] = a * up[e] * df;
-            up[e] = a * f;
-          }
-          *pg = pack4(ga);
-          *pu = pack4(up);
+        for (int e = 0; e < 4; ++e) {
+          const float a = acc[i][h][e];
+          float f, df;
+          act_and_grad<decltype(act)::value>(ga[e], f, df);
+          ga[e] = a * up[e] * df;
+          up[e] = a * f;
         }
+        *pg = pack4(ga);
+        *pu = pack4(up);
+      }
     };
     if (p.act == TE_ACT_SILU) gradients(std::integral_constant<int, TE_ACT_SILU>{});
     else gradients(std::integral_constant<int, TE_ACT_GELU>{});
     asm volatile("" ::: "memory");
-    store_rows<CH, ROWS>(region, to, ROWS * h, lane);
+    store_rows<CH, X::ROWS, kNonTemporal>(region, to, X::ROWS * h, lane);
     asm volatile("" ::: "memory");
   }
-}
-
-// A tile's accumulators to D (and aux / MXFP8 scales).
-template <class LY, bool BWD>
-__device__ __forceinline__ void finish_gated(v4f (&acc)[LY::FRN][LY::FRM], uint8_t* lds, const GatedParams& p,
-                                             const uint16_t* bias, int64_t m0, int64_t m_end, int64_t n0, int wave,
-                                             int lane) {
-  if constexpr (BWD) epilogue_dgated<LY>(acc, lds, p, m0, m_end, n0, wave, lane);
-  else epilogue_gated<LY>(acc, lds, p, bias, m0, m_end, n0, wave, lane);
 }
 
 // Output columns of a tile: a forward tile's B rows are gate and up rows of BN / 2 columns.
@@ -447,7 +459,13 @@ __device__ __forceinline__ void gated_tile(uint8_t* lds, const GatedParams& p, c
     const GatedOperand B = make_gated_operand<LY>(b, b_scale, n0, p.N, p.K, wave, lane);
     mainloop<LY, FA, FB, SM_MX, true>(lds, acc, A, B, p.K, wave, lane);
   }
-  finish_gated<LY, BWD>(acc, lds, p, bias, m0, m_end, n0, wave, lane);
+  if constexpr (BWD) {
+    DgatedAux<LY> aux;
+    aux.begin(p, m0, m_end, n0, wave, lane);
+    epilogue_dgated<LY>(acc, lds, p, aux, m0, m_end, n0, wave, lane);
+  } else {
+    epilogue_gated<LY>(acc, lds, p, bias, m0, m_end, n0, wave, lane);
+  }
 }
 
 template <class LY, int FA, int FB, bool BWD>

@@ -69,6 +69,8 @@ __global__ __launch_bounds__(Big4::kThreads, 1) void gated_gemm4_kernel(GatedPar
   for (;;) {
     v4f acc[LY::FRN][LY::FRM];
     mainloop4<FA, FB, SM_MX, true>(lds, acc, A, B, p.K, wave, a_blk, b_blk);
+    DgatedAux<LY> aux;
+    if constexpr (BWD) aux.begin(p, m0, p.M, n0, wave, lane_id_fresh());
     const int vn = v + (int)gridDim.x;
     int64_t m0n = 0, n0n = 0;
     Operand An = A;
@@ -77,7 +79,8 @@ __global__ __launch_bounds__(Big4::kThreads, 1) void gated_gemm4_kernel(GatedPar
       tile(vn, m0n, n0n, An, Bn);
       prologue4<SM_MX>(lds, An, Bn, p.K, wave, a_blk, b_blk);
     }
-    finish_gated<LY, BWD>(acc, lds + LY::kStage, p, p.bias, m0, p.M, n0, wave, lane_id_fresh());
+    if constexpr (BWD) epilogue_dgated<LY>(acc, lds + LY::kStage, p, aux, m0, p.M, n0, wave, lane_id_fresh());
+    else epilogue_gated<LY>(acc, lds + LY::kStage, p, p.bias, m0, p.M, n0, wave, lane_id_fresh());
     if (vn >= ntiles) break;
     v = vn;
     m0 = m0n;

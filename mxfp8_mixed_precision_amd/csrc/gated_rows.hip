@@ -17,7 +17,6 @@ namespace temx {
 namespace {
 
 constexpr int kUnroll = 4;  // K steps of a wave in flight
-constexpr int kCacheNt = 2;  // non-temporal: the weights are read once
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, kRsrcWord3);
@@ -66,7 +65,7 @@ __global__ __launch_bounds__(64 * W) void gated_rows_kernel(GatedParams p) {
 #pragma unroll
       for (int f = 0; f < 2 * NG; ++f) {
         const int row = (int)(16 * (f >> 1));
-        b[u][f] = load_frag<kCacheNt>(rb[f & 1], vo + (int)(row * K), so);
+        b[u][f] = load_frag<kNonTemporal>(rb[f & 1], vo + (int)(row * K), so);
         sb[u][f] = __builtin_amdgcn_raw_buffer_load_b8(rsb[f & 1], vs + (int)(row * ks), ss, 0);
       }
 #pragma unroll
