@@ -45,16 +45,25 @@ size_t gated_workspace(int64_t M, int64_t cols, int64_t K, int64_t N) {
   return four_wave_mx(M, cols, K) ? scale_blocks_bytes(M, cols, K) : 0;
 }
 
+// The few-row kernel instead of a tile: up to 64 rows; from 33 only where 128-row tiles would leave a quarter of the
+// CUs idle (N = 14336, K = 4096, 64 rows: 54 us against 35 with tiles; N = 8192, K = 8192: 55 against 57; N = 4096,
+// K = 4096: 16 against 29).
+bool few_rows(int64_t M, int64_t N) {
+  return M <= 32 || (M <= kFewRows && 4 * ((2 * N + 127) / 128) < 3 * (int64_t)device_cu_count());
+}
+
 template <bool BWD>
 te_status dense_gated(const GatedParams& p, te_dtype fa, te_dtype fb, void* workspace, size_t workspace_bytes,
                       hipStream_t stream) {
   const int64_t cols = BWD ? p.N : 2 * p.N;
-  if (!BWD && p.M <= kFewRows) return launch_gated_rows(p, fa, fb, stream);
+  if (!BWD && few_rows(p.M, p.N)) return launch_gated_rows(p, fa, fb, stream);
   const size_t want = gated_workspace(p.M, cols, p.K, p.N);
   if (want > 0 && workspace != nullptr && workspace_bytes >= want && ((uintptr_t)workspace & 255u) == 0 &&
       aligned16(p.a_scale) && aligned16(p.b_scale))
     return launch_gated4(p, BWD, fa, fb, workspace, stream);
-  if (use_small_tile(((p.M + 255) / 256) * ((cols + 255) / 256))) return launch_gated<Small, BWD>(p, fa, fb, stream);
+  const Tile t = pick_tile(p.M, cols, p.K);
+  if (t == Tile::SmallDeep) return launch_gated<SmallDeep, BWD>(p, fa, fb, stream);
+  if (t == Tile::Small) return launch_gated<Small, BWD>(p, fa, fb, stream);
   return launch_gated<Big, BWD>(p, fa, fb, stream);
 }
 
