@@ -10,6 +10,7 @@ the library has not been built (``python mxfp8_mixed_precision_amd/build.py``).
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -756,3 +757,69 @@ def fp8_block_gemm(a, a_scale_inv, a_fmt, b, b_scale_inv, b_fmt, b_block_2d=True
     te_fp8_block_gemm(a, a_scale_inv, a_fmt, b, b_scale_inv, b_fmt, b_block_2d, d, epilogue, bias, aux, mode,
                       workspace, stream, beta)
     return d, (aux if epilogue == "bias_gelu_aux" else None)
+
+
+def _allocating_on(stream, device):
+    """Context in which a helper's outputs and workspaces belong to the stream that its call runs on (memory freed by
+    the caller is then reused in that stream's order)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def norm_forward(kind, x, gamma, beta=None, eps=1e-5, residual=None, mx_fmt=None, want_y=True, stream=None):
+    """Layer norm ("layer") or RMS norm ("rms") of x [rows, cols] (+ residual) ->
+    (y, q, q_scale, sum, mean, rstd): y in x's dtype (None if not wanted), its MXFP8 operand with mx_fmt, the sum
+    with a residual (what norm_backward takes as x), the statistics (mean None for RMS norm)."""
+    rows, cols = x.shape
+    dev = x.device
+    with _allocating_on(stream, dev):
+        y = torch.empty_like(x) if want_y else None
+        q = torch.empty((rows, cols), dtype=torch.uint8, device=dev) if mx_fmt else None
+        qs = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev) if mx_fmt else None
+        total = torch.empty_like(x) if residual is not None else None
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+        mean = torch.empty_like(rstd) if NORM_KINDS[kind] == TE_NORM_LAYER else None
+        te_norm_forward(kind, x, gamma, beta, eps, y, q, qs, mx_fmt or "e4m3", residual, total, mean, rstd, stream)
+    return y, q, qs, total, mean, rstd
+
+
+def norm_backward(kind, dy, x, gamma, mean, rstd, dskip=None, want_dbeta=True, stream=None):
+    """-> (dx, dgamma, dbeta): dx + dskip where given; dbeta None for RMS norm or where not wanted."""
+    dev = x.device
+    with _allocating_on(stream, dev):
+        dx, dgamma = torch.empty_like(x), torch.empty_like(gamma)
+        dbeta = torch.empty_like(gamma) if want_dbeta and NORM_KINDS[kind] == TE_NORM_LAYER else None
+        size = te_norm_backward_workspace_size(*x.shape)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+        te_norm_backward(kind, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, dskip, ws, stream)
+    return dx, dgamma, dbeta
+
+
+def mxfp8_gated_gemm(a, a_scale, a_fmt, b, b_scale, b_fmt, activation="silu", bias=None, out_fmt=None, want_aux=False,
+                     stream=None):
+    """act(A Wg^T + bg) * (A Wu^T + bu) with b = [Wg; Wu] -> (D, d_scale, aux): D bf16, or with out_fmt MXFP8 codes
+    and their E8M0 scales; aux, the bf16 pre-activations [gate | up] that mxfp8_dgated_gemm takes, where wanted."""
+    M, N, K = a.shape[0], b.shape[0] // 2, a.shape[1]
+    dev = a.device
+    with _allocating_on(stream, dev):
+        d = torch.empty((M, N), dtype=torch.uint8 if out_fmt else torch.bfloat16, device=dev)
+        ds = torch.empty((M, N // 32), dtype=torch.uint8, device=dev) if out_fmt else None
+        aux = torch.empty((M, 2 * N), dtype=torch.bfloat16, device=dev) if want_aux else None
+        size = te_mxfp8_gated_gemm_workspace_size(M, N, K)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+        te_mxfp8_gated_gemm(a, a_scale, a_fmt, b, b_scale, b_fmt, d, activation, ds, out_fmt, bias, aux, ws, stream)
+    return d, ds, aux
+
+
+def mxfp8_dgated_gemm(a, a_scale, a_fmt, b, b_scale, b_fmt, aux, activation="silu", stream=None):
+    """[dgate | dup] bf16 [M, 2N] from the output gradient's GEMM A . B^T and the saved pre-activations aux."""
+    M, N, K = a.shape[0], b.shape[0], a.shape[1]
+    with _allocating_on(stream, a.device):
+        d = torch.empty((M, 2 * N), dtype=torch.bfloat16, device=a.device)
+        size = te_mxfp8_dgated_gemm_workspace_size(M, N, K)
+        ws = torch.empty(size, dtype=torch.uint8, device=a.device) if size else None
+        te_mxfp8_dgated_gemm(a, a_scale, a_fmt, b, b_scale, b_fmt, aux, d, activation, ws, stream)
+    return d
