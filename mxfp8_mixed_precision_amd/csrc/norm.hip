@@ -246,6 +246,7 @@ struct NormFwd {
   uint8_t* q_scale;
   float* mean;
   float* rstd;
+  int64_t row0;  // of the launch
   int64_t rows;
   int cols;
   float eps;
@@ -278,7 +279,7 @@ __global__ __launch_bounds__(NT* rows_at_a_time(NT, 256)) void norm_fwd_kernel(N
   __shared__ float2 all_slots[kRows][kWaves];
   float2(&slots)[kWaves] = all_slots[row_lane<NT>()];
   const int n = p.cols, t = threadIdx.x % NT;
-  const int64_t row = (int64_t)blockIdx.x * kRows + row_lane<NT>(), at = row * n;
+  const int64_t row = p.row0 + (int64_t)blockIdx.x * kRows + row_lane<NT>(), at = row * n;
   const bool row_ok = kRows == 1 || row < p.rows;  // every lane takes part in the exchanges below
   // A row past the end computes on the first and stores nothing.  sum_out may be one of the inputs: what a tail's or
   // such a row's load may see changed is not used.
@@ -393,7 +394,7 @@ template <class T, class W>
 __global__ __launch_bounds__(kWideThreads) void norm_fwd_wide_kernel(NormFwd p) {
   __shared__ float slots[kWideThreads / 64];
   const int n = p.cols, nch = (n + kChunk - 1) / kChunk;
-  const int64_t row = blockIdx.x, at = row * n;
+  const int64_t row = p.row0 + blockIdx.x, at = row * n;
   const T* x = static_cast<const T*>(p.x) + at;
   float mean = 0.f;
   if (p.layer || p.residual) {
@@ -468,6 +469,7 @@ struct NormBwd {
   void* dgamma;
   void* dbeta;        // NULL: not wanted
   float* part;        // [tiles][cols] of dgamma, then of dbeta
+  int64_t row0;       // of the launch (wide kernel)
   int64_t rows;
   int cols;
   int tiles;
@@ -583,7 +585,7 @@ template <class T, class W>
 __global__ __launch_bounds__(kWideThreads) void norm_bwd_wide_kernel(NormBwd p) {
   __shared__ float slots[2][kWideThreads / 64];
   const int n = p.cols, nch = (n + kChunk - 1) / kChunk;
-  const int64_t row = blockIdx.x, at = row * n;
+  const int64_t row = p.row0 + blockIdx.x, at = row * n;
   const float mean = p.mean ? p.mean[row] : 0.f, rstd = p.rstd[row];
   const T* x = static_cast<const T*>(p.x) + at;
   const T* dy = static_cast<const T*>(p.dy) + at;
@@ -738,15 +740,28 @@ bool with_threads(int nt, F f) {
 
 bool float_dtype(te_dtype t) { return t == TE_BF16 || t == TE_FP16 || t == TE_FP32; }
 
+// f(workgroups) for launches of `each` rows per workgroup, p.row0 their first row: a launch holds fewer than 2^32
+// threads.
+template <class P, class F>
+void for_launches(P& p, int each, F f) {
+  constexpr int64_t kMost = (int64_t)1 << 21;  // workgroups of up to 1024 threads
+  const int64_t blocks = (p.rows + each - 1) / each;
+  for (int64_t b = 0; b < blocks; b += kMost) {
+    p.row0 = b * each;
+    f((unsigned)(blocks - b < kMost ? blocks - b : kMost));
+  }
+}
+
 // Forward: a wave (or less) per row up to 256 chunks and 256 threads up to 1024, up to 4 chunks per thread: several
 // rows' loads are in flight per CU and few waves have to meet (8192 x 8192 bf16: 52 us with 256 x 4, 76 with
 // 1024 x 1; 8192 x 4096: 29 and 35).  At most a row per CU takes a thread per chunk instead (1 x 8192: 3.8 us).
 template <class T, class W>
-te_status run_fwd(const NormFwd& p, hipStream_t stream) {
+te_status run_fwd(NormFwd p, hipStream_t stream) {
   auto go = [&](auto nt, auto nc) {
     constexpr int NT = decltype(nt)::value, NC = decltype(nc)::value, kRows = rows_at_a_time(NT, 256);
-    hipLaunchKernelGGL((norm_fwd_kernel<T, W, NT, NC>), dim3((unsigned)((p.rows + kRows - 1) / kRows)),
-                       dim3(NT * kRows), 0, stream, p);
+    for_launches(p, kRows, [&](unsigned blocks) {
+      hipLaunchKernelGGL((norm_fwd_kernel<T, W, NT, NC>), dim3(blocks), dim3(NT * kRows), 0, stream, p);
+    });
   };
   using std::integral_constant;
   const int ch = (int)(((int64_t)p.cols + kChunk - 1) / kChunk);
@@ -764,12 +779,15 @@ te_status run_fwd(const NormFwd& p, hipStream_t stream) {
   else if (ch <= 1024) go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
   else if (ch <= 2048) go(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
   else if (ch <= 4096) go(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
-  else hipLaunchKernelGGL((norm_fwd_wide_kernel<T, W>), dim3((unsigned)p.rows), dim3(kWideThreads), 0, stream, p);
+  else
+    for_launches(p, 1, [&](unsigned blocks) {
+      hipLaunchKernelGGL((norm_fwd_wide_kernel<T, W>), dim3(blocks), dim3(kWideThreads), 0, stream, p);
+    });
   return launch_status();
 }
 
 template <class T, class W>
-te_status run_bwd(const NormBwd& p, hipStream_t stream) {
+te_status run_bwd(NormBwd p, hipStream_t stream) {
   const dim3 tiles((unsigned)p.tiles);
   if (p.rows > 0) {
     const int nt = bwd_threads_per_row(p.cols);
@@ -784,7 +802,9 @@ te_status run_bwd(const NormBwd& p, hipStream_t stream) {
       hipLaunchKernelGGL((norm_bwd_kernel<T, W, 256, NT>), tiles, dim3(NT * rows_at_a_time(NT, 256)), 0, stream, p);
     });
     if (!held) {
-      hipLaunchKernelGGL((norm_bwd_wide_kernel<T, W>), dim3((unsigned)p.rows), dim3(kWideThreads), 0, stream, p);
+      for_launches(p, 1, [&](unsigned blocks) {
+        hipLaunchKernelGGL((norm_bwd_wide_kernel<T, W>), dim3(blocks), dim3(kWideThreads), 0, stream, p);
+      });
       hipLaunchKernelGGL((norm_bwd_columns_kernel<T>),
                          dim3((unsigned)((p.cols + kColChunks * kChunk - 1) / (kColChunks * kChunk)),
                               (unsigned)p.tiles),
@@ -844,8 +864,8 @@ extern "C" te_status te_norm_forward(te_norm_kind kind, const void* x, te_dtype 
                  aligned16(y) && aligned16(q) && aligned4(mean) && aligned4(rstd),
              TE_ERR_ALIGN);
   TE_REQUIRE(device_is_gfx950(), TE_ERR_ARCH);
-  const NormFwd p{x,    residual, gamma, beta, sum_out,   y,   q, q_scale, mean, rstd,
-                  rows, (int)cols, eps,  kind == TE_NORM_LAYER, q_fmt == TE_E5M2};
+  const NormFwd p{x, residual, gamma, beta, sum_out,   y,   q,  q_scale, mean,
+                  rstd, 0,     rows,  (int)cols, eps, kind == TE_NORM_LAYER, q_fmt == TE_E5M2};
   TEMX_NORM_TYPES(run_fwd)
 }
 
@@ -873,7 +893,7 @@ extern "C" te_status te_norm_backward(te_norm_kind kind, const void* dy, const v
     TE_REQUIRE(workspace_bytes >= te_norm_backward_workspace_size(rows, cols), TE_ERR_WORKSPACE);
   }
   TE_REQUIRE(device_is_gfx950(), TE_ERR_ARCH);
-  const NormBwd p{dy, x, dskip, gamma, mean, rstd, dx, dgamma, dbeta, static_cast<float*>(workspace), rows, (int)cols,
+  const NormBwd p{dy, x, dskip, gamma, mean, rstd, dx, dgamma, dbeta, static_cast<float*>(workspace), 0, rows, (int)cols,
                   rows > 0 ? norm_tiles(rows, cols) : 0};
   TEMX_NORM_TYPES(run_bwd)
 }

@@ -302,3 +302,20 @@ def test_gradients_against_differences_of_the_forward(kind):
         h = 2.0 ** -6
         d1, d2 = (at(h) - at(-h)) / (2 * h), (at(2 * h) - at(-2 * h)) / (4 * h)
         assert abs(d1 - got) <= noise / h + abs(d2 - d1) + 1e-5 * abs(got)
+
+
+def test_more_rows_than_one_launch_holds():
+    rows = (1 << 25) + 5  # 2^21 workgroups of 16 rows, and a second launch
+    x = torch.randn((rows, 2), device="cuda")
+    gamma, beta = weights(8, 2, torch.float32)
+    o = forward(x, gamma, beta, "layer")
+    for sl in (slice(0, 40), slice((1 << 25) - 20, rows)):
+        want = forward(x[sl].clone(), gamma, beta, "layer")
+        for k in ("y", "mean", "rstd"):
+            assert torch.equal(o[k][sl], want[k])
+    dx, dg, db = backward(x, x, gamma, o["mean"], o["rstd"], "layer")
+    want = backward(x[-20:].clone(), x[-20:].clone(), gamma, o["mean"][-20:].clone(), o["rstd"][-20:].clone(), "layer")
+    assert torch.equal(dx[-20:], want[0])
+    # dbeta: exact to the paths' rounding (at most 100 + rows / 32 additions, here far fewer: rows / 16384 + 200)
+    bound = (rows / 16384 + 200) * U * x.double().abs().sum(0)
+    assert ((db.double() - x.double().sum(0)).abs() <= bound).all()
