@@ -132,6 +132,13 @@ __device__ __forceinline__ Raw<T> load_chunk(const T* row, int c, int n) {
   return r;
 }
 
+// The chunk's registers as values the compiler knows nothing about.
+template <class T>
+__device__ __forceinline__ void opaque(Raw<T>& r) {
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(r.w) / 4; ++i) asm volatile("" : "+v"(r.w[i]));
+}
+
 template <class T>
 __device__ __forceinline__ void unpack(const Raw<T>& r, float (&f)[kChunk]) {
 #pragma unroll
@@ -478,28 +485,36 @@ struct NormBwd {
 // Rows held in registers as in norm_fwd_kernel, a chunk per thread; each workgroup walks rows and keeps its columns' sums of dy xh and
 // dy in registers, so dy and x are read once for dx and for the weights' gradients.  The next rows' loads are in
 // flight while a row is computed.  At the end a workgroup's row lanes join in LDS and leave one row of partial sums.
-template <class T, class W, int THREADS, int NT>
+template <class T, class W, int THREADS, int NT, int NC = 1>
 __global__ __launch_bounds__(NT* rows_at_a_time(NT, THREADS)) void norm_bwd_kernel(NormBwd p) {
   constexpr int kRows = rows_at_a_time(NT, THREADS), kWaves = NT > 64 ? NT / 64 : 1, kLanes = NT < 64 ? NT : 64;
+  constexpr bool kAhead = NC == 1;  // the next rows' loads in flight (more chunks leave no registers for them)
   __shared__ float2 slots[2][kRows * kWaves];
   __shared__ float joined[kRows > 1 ? kRows - 1 : 1][kRows > 1 ? NT * kChunk : 1];
   const int n = p.cols, t = threadIdx.x % NT, sub = row_lane<NT>();
   const bool layer = p.mean != nullptr, skip = p.dskip != nullptr;
-  const int c = t * kChunk;
-  Raw<W> gamma = load_chunk(static_cast<const W*>(p.gamma), c, n);
-  float dg[kChunk], db[kChunk];
+  auto col = [&](int j) { return (t + j * NT) * kChunk; };
+  Raw<W> gamma[NC];
+  float dg[NC][kChunk], db[NC][kChunk];
 #pragma unroll
-  for (int e = 0; e < kChunk; ++e) dg[e] = db[e] = 0.f;
+  for (int j = 0; j < NC; ++j) {
+    gamma[j] = load_chunk(static_cast<const W*>(p.gamma), col(j), n);
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e) dg[j][e] = db[j][e] = 0.f;
+  }
   struct Row {
-    Raw<T> x, dy, skip;
+    Raw<T> x[NC], dy[NC], skip[NC];
     float mean, rstd;
   };
   auto load = [&](Row& v, int64_t row) __attribute__((always_inline)) {
     row = min(row, p.rows - 1);  // a row past the end: the last one again, used for nothing
     const int64_t at = row * n;
-    v.x = load_ahead(static_cast<const T*>(p.x) + at, c, n);
-    v.dy = load_ahead(static_cast<const T*>(p.dy) + at, c, n);
-    if (skip) v.skip = load_ahead(static_cast<const T*>(p.dskip) + at, c, n);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      v.x[j] = load_ahead(static_cast<const T*>(p.x) + at, col(j), n);
+      v.dy[j] = load_ahead(static_cast<const T*>(p.dy) + at, col(j), n);
+      if (skip) v.skip[j] = load_ahead(static_cast<const T*>(p.dskip) + at, col(j), n);
+    }
     v.mean = layer ? p.mean[row] : 0.f;
     v.rstd = p.rstd[row];
   };
@@ -510,27 +525,37 @@ __global__ __launch_bounds__(NT* rows_at_a_time(NT, THREADS)) void norm_bwd_kern
   load(now, base + sub);
   int buf = 0;
   for (; base < p.rows; base += step, buf ^= 1) {
-    if (base + step < p.rows) load(next, base + step + sub);  // in flight through this row
+    if constexpr (kAhead)
+      if (base + step < p.rows) load(next, base + step + sub);
     float s1 = 0.f, s2 = 0.f;
     const bool row_ok = base + sub < p.rows;
-    settle<T>(now.x, c, n);
-    settle<T>(now.dy, c, n);
     float xh[kChunk], d[kChunk], g[kChunk];
-    unpack<T>(now.x, xh);
-    unpack<T>(now.dy, d);
-    unpack<W>(gamma, g);
-#pragma unroll
-    for (int e = 0; e < kChunk; ++e) {
-      xh[e] = (xh[e] - now.mean) * now.rstd;
-      g[e] *= d[e];
-      s1 += g[e];
-      s2 = __builtin_fmaf(g[e], xh[e], s2);
-    }
-    if (row_ok) {
+    auto terms = [&](int j) __attribute__((always_inline)) {  // xh, dy and g of chunk j
+      unpack<T>(now.x[j], xh);
+      unpack<T>(now.dy[j], d);
+      unpack<W>(gamma[j], g);
 #pragma unroll
       for (int e = 0; e < kChunk; ++e) {
-        dg[e] = __builtin_fmaf(d[e], xh[e], dg[e]);
-        db[e] += d[e];
+        xh[e] = (xh[e] - now.mean) * now.rstd;
+        g[e] *= d[e];
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      settle<T>(now.x[j], col(j), n);
+      settle<T>(now.dy[j], col(j), n);
+      terms(j);
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) {
+        s1 += g[e];
+        s2 = __builtin_fmaf(g[e], xh[e], s2);
+      }
+      if (row_ok) {
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e) {
+          dg[j][e] = __builtin_fmaf(d[e], xh[e], dg[j][e]);
+          db[j][e] += d[e];
+        }
       }
     }
     s1 = lanes_sum<kLanes>(s1);
@@ -549,34 +574,46 @@ __global__ __launch_bounds__(NT* rows_at_a_time(NT, THREADS)) void norm_bwd_kern
     s1 = layer ? s1 * inv_n : 0.f;
     s2 *= inv_n;
 #pragma unroll
-    for (int e = 0; e < kChunk; ++e) g[e] = now.rstd * (g[e] - s1 - xh[e] * s2);
-    if (skip) {
-      settle<T>(now.skip, c, n);
-      unpack<T>(now.skip, d);
+    for (int j = 0; j < NC; ++j) {
+      if constexpr (NC > 1) {  // formed again: kept, the chunks' terms do not fit the registers
+        opaque(now.x[j]);
+        opaque(now.dy[j]);
+        terms(j);
+      }
 #pragma unroll
-      for (int e = 0; e < kChunk; ++e) g[e] += d[e];
+      for (int e = 0; e < kChunk; ++e) g[e] = now.rstd * (g[e] - s1 - xh[e] * s2);
+      if (skip) {
+        settle<T>(now.skip[j], col(j), n);
+        unpack<T>(now.skip[j], d);
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e) g[e] += d[e];
+      }
+      if (row_ok) store_chunk(static_cast<T*>(p.dx) + (base + sub) * n + col(j), pack<T>(g), n - col(j));
     }
-    if (row_ok) store_chunk(static_cast<T*>(p.dx) + (base + sub) * n + c, pack<T>(g), n - c);
-    now = next;
+    if constexpr (kAhead) now = next;
+    else if (base + step < p.rows) load(now, base + step + sub);
   }
   // the row lanes' sums in order, one 8-column chunk per thread at a time
   float* part = p.part + (int64_t)blockIdx.x * n;
   for (int pass = 0; pass < (p.dbeta != nullptr ? 2 : 1); ++pass) {
-    float v[kChunk];
 #pragma unroll
-    for (int e = 0; e < kChunk; ++e) v[e] = pass ? db[e] : dg[e];
-    if constexpr (kRows > 1) {
-      __syncthreads();
-      if (sub > 0)
+    for (int j = 0; j < NC; ++j) {
+      float v[kChunk];
 #pragma unroll
-        for (int e = 0; e < kChunk; ++e) joined[sub - 1][e * NT + t] = v[e];
-      __syncthreads();
-      if (sub == 0)
-        for (int w = 0; w < kRows - 1; ++w)
+      for (int e = 0; e < kChunk; ++e) v[e] = pass ? db[j][e] : dg[j][e];
+      if constexpr (kRows > 1) {
+        __syncthreads();
+        if (sub > 0)
 #pragma unroll
-          for (int e = 0; e < kChunk; ++e) v[e] += joined[w][e * NT + t];
+          for (int e = 0; e < kChunk; ++e) joined[sub - 1][e * NT + t] = v[e];
+        __syncthreads();
+        if (sub == 0)
+          for (int w = 0; w < kRows - 1; ++w)
+#pragma unroll
+            for (int e = 0; e < kChunk; ++e) v[e] += joined[w][e * NT + t];
+      }
+      if (sub == 0) store_chunk(part + (int64_t)pass * p.tiles * n + col(j), pack<float>(v), n - col(j));
     }
-    if (sub == 0) store_chunk(part + (int64_t)pass * p.tiles * n + c, pack<float>(v), n - c);
   }
 }
 
@@ -713,7 +750,7 @@ inline int bwd_threads(int nt, int64_t rows) {
 inline int norm_tiles(int64_t rows, int64_t cols) {
   const int nt = bwd_threads_per_row(cols);
   const int64_t cus = device_cu_count();
-  const int64_t per = nt == 0 ? 32 : rows_at_a_time(nt, bwd_threads(nt, rows));  // rows at a time
+  const int64_t per = nt == 0 ? (cols <= 2048 * kChunk ? 1 : 32) : rows_at_a_time(nt, bwd_threads(nt, rows));  // rows at a time
   const int64_t most = nt == 0 || nt * per > 640 ? cus : 2 * cus;
   const int64_t t = (rows + per - 1) / per;
   return (int)(t < most ? t : most);
@@ -791,7 +828,7 @@ te_status run_bwd(NormBwd p, hipStream_t stream) {
   const dim3 tiles((unsigned)p.tiles);
   if (p.rows > 0) {
     const int nt = bwd_threads_per_row(p.cols);
-    const bool held = with_threads(nt, [&](auto n) {
+    bool held = with_threads(nt, [&](auto n) {
       constexpr int NT = decltype(n)::value;
       if constexpr (rows_at_a_time(NT, 1024) > 1)
         if (bwd_threads(nt, p.rows) == 1024) {
@@ -801,6 +838,13 @@ te_status run_bwd(NormBwd p, hipStream_t stream) {
         }
       hipLaunchKernelGGL((norm_bwd_kernel<T, W, 256, NT>), tiles, dim3(NT * rows_at_a_time(NT, 256)), 0, stream, p);
     });
+    // up to 2048 chunks of 2-byte elements: four per thread (4096 x 16384 bf16: 96 us, 151 with the wide kernels)
+    if constexpr (sizeof(T) == 2) {
+      if (!held && p.cols <= 2048 * kChunk) {
+        hipLaunchKernelGGL((norm_bwd_kernel<T, W, 512, 512, 4>), tiles, dim3(512), 0, stream, p);
+        held = true;
+      }
+    }
     if (!held) {
       for_launches(p, 1, [&](unsigned blocks) {
         hipLaunchKernelGGL((norm_bwd_wide_kernel<T, W>), dim3(blocks), dim3(kWideThreads), 0, stream, p);
