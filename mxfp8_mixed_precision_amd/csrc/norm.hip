@@ -480,9 +480,10 @@ struct NormBwd {
   int64_t rows;
   int cols;
   int tiles;
+  int col0;           // of the launch (final kernel)
 };
 
-// Rows held in registers as in norm_fwd_kernel, a chunk per thread; each workgroup walks rows and keeps its columns' sums of dy xh and
+// Rows held in registers as in norm_fwd_kernel; each workgroup walks rows and keeps its columns' sums of dy xh and
 // dy in registers, so dy and x are read once for dx and for the weights' gradients.  The next rows' loads are in
 // flight while a row is computed.  At the end a workgroup's row lanes join in LDS and leave one row of partial sums.
 template <class T, class W, int THREADS, int NT, int NC = 1>
@@ -707,7 +708,7 @@ template <class W>
 __global__ __launch_bounds__(kFinCols* kFinLanes) void norm_bwd_final_kernel(NormBwd p) {
   __shared__ float red[kFinLanes][kFinCols + 1];
   const int cx = threadIdx.x % kFinCols, ty = threadIdx.x / kFinCols;
-  const int col = blockIdx.x * kFinCols + cx;
+  const int col = p.col0 + blockIdx.x * kFinCols + cx;
   const float* part = p.part + (int64_t)blockIdx.y * p.tiles * p.cols;
   float s = 0.f;
   if (col < p.cols) {
@@ -855,9 +856,14 @@ te_status run_bwd(NormBwd p, hipStream_t stream) {
                          dim3(kColThreads), 0, stream, p);
     }
   }
-  hipLaunchKernelGGL((norm_bwd_final_kernel<W>),
-                     dim3((unsigned)((p.cols + kFinCols - 1) / kFinCols), p.dbeta ? 2u : 1u),
-                     dim3(kFinCols * kFinLanes), 0, stream, p);
+  constexpr int64_t kMost = (int64_t)1 << 21;  // workgroups per launch, as in for_launches
+  const int64_t blocks = ((int64_t)p.cols + kFinCols - 1) / kFinCols;
+  for (int64_t b = 0; b < blocks; b += kMost) {
+    p.col0 = (int)(b * kFinCols);
+    hipLaunchKernelGGL((norm_bwd_final_kernel<W>),
+                       dim3((unsigned)(blocks - b < kMost ? blocks - b : kMost), p.dbeta ? 2u : 1u),
+                       dim3(kFinCols * kFinLanes), 0, stream, p);
+  }
   return launch_status();
 }
 

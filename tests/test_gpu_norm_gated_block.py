@@ -225,6 +225,17 @@ def test_norms_past_32_bit_offsets():
     torch.cuda.empty_cache()
 
 
+def test_norm_backward_of_a_row_longer_than_one_launch_of_columns():
+    cols = 2 ** 26 + 40
+    m = te()
+    x, dy = randn(1, 1, 1024).repeat(1, 65_537)[:, :cols].contiguous(), torch.ones((1, cols), **BF)
+    mean, rstd = torch.zeros(1, device="cuda"), torch.ones(1, device="cuda")
+    _, dgamma, dbeta = m.norm_backward("layer", dy, x, torch.ones(cols, **BF), mean, rstd)
+    assert torch.equal(dgamma, x[0]) and torch.equal(dbeta, dy[0])  # one row: dy xh and dy themselves
+    del x, dy, dgamma, dbeta
+    torch.cuda.empty_cache()
+
+
 def test_gated_gemms_past_32_bit_offsets():
     M, N, K = 140_100, 8_192, 128  # 2.3e9 pre-activations
     m = te()
