@@ -479,54 +479,98 @@ __global__ __launch_bounds__(LY::kThreads) void gated_gemm_kernel(GatedParams p)
   gated_tile<LY, FA, FB, BWD>(lds, p, p.b, p.b_scale, p.bias, (int64_t)tm * LY::BM, p.M, (int64_t)tn * BN, wave, lane);
 }
 
-// Grouped: a persistent grid walks the flat list of (expert row-tile, n-tile)
-// pairs, built in LDS from the device-resident splits.  Rows behind the last
-// group belong to no tile and stay as they were.
+// Grouped: a persistent grid walks the flat list of (expert row-tile, n-tile) pairs, built in LDS from the
+// device-resident splits.  Rows behind the last group belong to no tile and stay as they were.
+// A tail tile (TailTile) holds an expert's last rows where at most half of a big tile's are left: half the MFMAs
+// and three quarters of the copies.  Where all experts' weights fit the 256 MB MALL, an XCD's whole tiles come first
+// and its tails last, which evens the last round out; larger weights would be fetched from HBM for each, so there a
+// tail follows its expert's whole tiles and runs beside them.  Measured, us, forward / backward (without tail tiles;
+// tails last; tails next to their expert's):
+//   16 ragged experts, 8192 rows, N = K = 2048      105 / 88   100 / 78   107 / 89   (weights 134 / 67 MB)
+//   8 experts of 600 rows, N = 4096, K = 1024        62 / 65    61 / 58    61 / 58   (67 / 34 MB)
+//   32 experts of 290 rows, N = 1536, K = 4096      187 / 141  201 / 132  174 / 142  (403 / 201 MB)
+//   16 experts of 40..800 rows, N = K = 4096        354 / 203  355 / 213  343 / 190  (537 / 268 MB)
+template <class LY>
+struct TailTile {
+  static constexpr bool kHas = false;
+  using type = LY;
+};
+template <>
+struct TailTile<Big> {
+  static constexpr bool kHas = true;
+  using type = Cfg<128, 256, 2, 4, 4, 2, 4>;
+};
+
 template <class LY, int FA, int FB, bool BWD>
 __global__ __launch_bounds__(LY::kThreads) void grouped_gated_gemm_kernel(GatedParams p) {
+  using Tail = typename TailTile<LY>::type;
+  constexpr bool kTails = TailTile<LY>::kHas;
   constexpr int BM = LY::BM, BN = tile_cols<LY, BWD>();
+  static_assert(Tail::kLds <= LY::kLds && Tail::kThreads == LY::kThreads && tile_cols<Tail, BWD>() == BN, "tail tile");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[LY::kLds];
-  __shared__ int tile_prefix[kMaxGroups + 1];
+  __shared__ int prefix[kTails ? 2 : 1][kMaxGroups + 1];  // whole tiles, tail tiles of the experts before e
   __shared__ int row_off[kMaxGroups + 1];
-  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int G = p.groups;
   for (int e = threadIdx.x; e < G; e += LY::kThreads) row_off[e + 1] = p.m_splits[e];
   __syncthreads();
   if (threadIdx.x == 0) {
-    int tiles = 0, off = 0;
-    tile_prefix[0] = 0;
-    row_off[0] = 0;
+    int whole = 0, tails = 0, off = 0;
+    row_off[0] = prefix[0][0] = 0;
+    if constexpr (kTails) prefix[1][0] = 0;
     for (int e = 0; e < G; ++e) {
       const int me = max(row_off[e + 1], 0);
       const int end = (int)min((int64_t)off + me, p.M);  // bad splits stay inside the tensors
-      tiles += (end - off + BM - 1) / BM;
+      const int rows = end - off, left = rows % BM;
+      const bool tail = kTails && left > 0 && left <= Tail::BM;
+      whole += rows / BM + (left > 0 && !tail ? 1 : 0);
+      tails += tail ? 1 : 0;
       off = end;
-      tile_prefix[e + 1] = tiles;
+      prefix[0][e + 1] = whole;
+      if constexpr (kTails) prefix[1][e + 1] = tails;
       row_off[e + 1] = off;
     }
   }
   __syncthreads();
   const int ntn = (int)((p.N + BN - 1) / BN);
-  const int total = tile_prefix[G] * ntn;
-  const int xcd = blockIdx.x % 8, slot = blockIdx.x / 8, nslots = gridDim.x / 8;
-  const int chunk = (total + 7) / 8;
-  const int t_end = min((xcd + 1) * chunk, total);
-  for (int t = xcd * chunk + slot; t < t_end; t += nslots) {
-    const int rt = t / ntn, tn = t % ntn;
-    int lo = 0, hi = G;  // the expert e with tile_prefix[e] <= rt < tile_prefix[e + 1]
+  const int xcd = blockIdx.x % 8, nslots = gridDim.x / 8;
+  // the XCD's share of `tiles` row tiles: items [from, from + n)
+  struct Share {
+    int from, n;
+  };
+  auto share = [&](int tiles) __attribute__((always_inline)) {
+    const int total = __builtin_amdgcn_readfirstlane(tiles) * ntn, chunk = (total + 7) / 8;
+    return Share{xcd * chunk, max(min(chunk, total - xcd * chunk), 0)};
+  };
+  const bool apart = kTails && (BWD ? 1 : 2) * (int64_t)G * p.N * p.K < (int64_t)256 << 20;
+  const int tails = kTails ? prefix[1][G] : 0;
+  const Share first = share(prefix[0][G] + (apart ? 0 : tails)), second = apart ? share(tails) : Share{0, 0};
+  for (int i = blockIdx.x / 8; i < first.n + second.n; i += nslots) {
+    const bool behind = i >= first.n;
+    const int item = behind ? second.from + i - first.n : first.from + i;
+    const int rt = item / ntn, tn = item % ntn;
+    auto before = [&](int e) __attribute__((always_inline)) {  // the list's row tiles of the experts before e
+      if constexpr (!kTails) return prefix[0][e];
+      else return apart ? prefix[behind][e] : prefix[0][e] + prefix[1][e];
+    };
+    int lo = 0, hi = G;  // the expert e with before(e) <= rt < before(e + 1)
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (tile_prefix[mid] <= rt) lo = mid; else hi = mid;
+      if (before(mid) <= rt) lo = mid; else hi = mid;
     }
     const int e = __builtin_amdgcn_readfirstlane(lo);
-    const int64_t m0 = __builtin_amdgcn_readfirstlane(row_off[e]) +
-                       (int64_t)(rt - __builtin_amdgcn_readfirstlane(tile_prefix[e])) * BM;
+    const int whole = __builtin_amdgcn_readfirstlane(prefix[0][e + 1] - prefix[0][e]);
+    const int at = behind ? whole : __builtin_amdgcn_readfirstlane(rt - before(e));  // a tail follows the whole tiles
+    const int64_t m0 = __builtin_amdgcn_readfirstlane(row_off[e]) + (int64_t)at * BM;
     const int64_t m_end = __builtin_amdgcn_readfirstlane(row_off[e + 1]);
-    const int64_t rows_b = (int64_t)e * p.N * (BWD ? 1 : 2);
+    const int64_t n0 = (int64_t)tn * BN, rows_b = (int64_t)e * p.N * (BWD ? 1 : 2);
+    const uint8_t* b = p.b + rows_b * p.K;
+    const uint8_t* b_scale = p.b_scale + rows_b * (p.K / 32);
+    const uint16_t* bias = p.bias ? p.bias + rows_b : nullptr;
+    const int lane = lane_id_fresh();  // so that no tile's lane offsets are kept live through the other's
     __syncthreads();  // the previous tile's reads of the LDS are done
-    gated_tile<LY, FA, FB, BWD>(lds, p, p.b + rows_b * p.K, p.b_scale + rows_b * (p.K / 32),
-                                p.bias ? p.bias + rows_b : nullptr, m0, m_end, (int64_t)tn * BN, wave, lane);
+    if (kTails && at == whole) gated_tile<Tail, FA, FB, BWD>(lds, p, b, b_scale, bias, m0, m_end, n0, wave, lane);
+    else gated_tile<LY, FA, FB, BWD>(lds, p, b, b_scale, bias, m0, m_end, n0, wave, lane);
   }
 }
 
