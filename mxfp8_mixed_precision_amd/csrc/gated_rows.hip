@@ -10,11 +10,12 @@
 // LDS and are added in wave order (deterministic); bias, activation, product
 // and the MXFP8 encode follow.  All reads go through buffer resources: rows
 // past M and K steps past the end read zeros.
+// Measured on MI355X, one row, N = 14336, K = 4096: 25.3 us, 121 MB of weights
+// and scales at 4.8 TB/s (a large copy: 5.1).
 #include "gated_core.h"
 
 namespace temx {
 namespace {
-
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, kRsrcWord3);

