@@ -749,12 +749,16 @@ inline int bwd_threads_per_row(int64_t cols) {
   return 0;
 }
 
-// Threads of a backward workgroup: 1024 where that leaves a workgroup for every CU, else 256 (or the row's).
+// Threads of a backward workgroup: 1024 where that leaves a workgroup for every CU, else 256 (or the row's).  Bf16, us,
+// 1024 and 256 threads: 16384 x 2048 41.2 and 45.1, 16384 x 1024 25.2 and 26.8, 131072 x 512 77.7 and 80.3; with few
+// rows, 2048 x 512, 13.4 and 11.6.
 inline int bwd_threads(int nt, int64_t rows) {
   return rows * nt >= (int64_t)device_cu_count() * 1024 ? 1024 : 256;
 }
 
 // Rows of partial sums of each weight gradient: the register kernel's workgroups, or the wide kernels' row tiles.
+// One workgroup of more than 640 threads per CU, two smaller ones (two of 1024 leave twice the partial sums: 16384 x
+// 2048 44.0 us and not 41.3, 8192 x 8192 85.4 and 78.5).
 inline int norm_tiles(int64_t rows, int64_t cols) {
   const int nt = bwd_threads_per_row(cols);
   const int64_t cus = device_cu_count();
