@@ -406,3 +406,20 @@ def test_grouped_tail_tiles_equal_the_dense_call(G, N, K, behind):
             assert torch.equal(back[:c], dd[off:off + c]), e
         off += c
     assert (d[used:] == 0x55).all() and (aux[used:] == 0x55).all() and (dd[used:] == 0x55).all()
+
+
+@pytest.mark.parametrize("N", [80, 4176])  # the small tile and the large one
+def test_grouped_splits_past_the_rows_stay_inside(N):
+    m = te()
+    K, total = 128, 1200
+    a, b = quantized(9, total, K), quantized(10, 3 * 2 * N, K, sigma=0.05)
+    pre = torch.randn((total, 2 * N), device="cuda").bfloat16()
+    got = []
+    for counts in ([700, 0, 500], [700, -5, 2 ** 31 - 1]):
+        splits = torch.tensor(counts, dtype=torch.int32, device="cuda")
+        d = torch.empty((total, N), dtype=torch.int16, device="cuda")
+        dd = torch.empty((total, 2 * N), dtype=torch.int16, device="cuda")
+        m.te_mxfp8_grouped_gated_gemm(splits, *a, "e4m3", *b, "e4m3", N, d, "silu")
+        m.te_mxfp8_grouped_dgated_gemm(splits, *a, "e4m3", *[t[:3 * N] for t in b], "e4m3", N, pre, dd, "silu")
+        got.append((d, dd))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
