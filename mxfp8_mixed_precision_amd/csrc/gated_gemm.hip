@@ -151,8 +151,12 @@ te_status grouped_gated(GatedParams p, te_dtype a_fmt, te_dtype b_fmt, hipStream
   TE_REQUIRE(device_is_gfx950(), TE_ERR_ARCH);
   const int cus = device_cu_count();
   const unsigned grid = cus < 8 ? 8u : (unsigned)(cus / 8 * 8);
-  // the splits stay on the device: the big-tile count is estimated from the total rows, one ragged tail per group
-  if (use_small_tile((p.M / 256 + p.groups) * ((cols + 255) / 256)))
+  // The splits stay on the device.  Groups of at most a small tile's rows on average take that tile: the weights bound
+  // them, and its grid is 4 times as fine (big and small tile, us, forward / backward: N = K = 2048, 8 rows over 64
+  // groups 26 / 29 and 20 / 22, 16 groups of 40 rows 35 / 25 and 33 / 20, 16 of 200 rows 43 / 46 and 55 / 38; 32 groups
+  // of 64 rows, N = 1536, K = 4096, 123 / 70 and 113 / 71).  Else by the big-tile count, estimated from the total rows
+  // and one ragged tail per group.
+  if (p.M <= 128 * (int64_t)p.groups || use_small_tile((p.M / 256 + p.groups) * ((cols + 255) / 256)))
     return launch_grouped_gated<Small, BWD>(p, a_fmt, b_fmt, 2 * grid, stream);
   return launch_grouped_gated<Big, BWD>(p, a_fmt, b_fmt, grid, stream);
 }
