@@ -477,8 +477,10 @@ te_status te_norm_forward(te_norm_kind kind, const void* x, te_dtype dtype, int6
  *                TE_NORM_RMS)
  *   workspace    device scratch of at least
  *                te_norm_backward_workspace_size(rows, cols) bytes, 16-byte
- *                aligned: fp32 partial sums of the weight gradients.  Calls
- *                that may run at the same time need workspaces of their own.
+ *                aligned: fp32 partial sums of the weight gradients.  The size
+ *                never falls as rows or cols grow: one workspace of a program's
+ *                longest and widest call serves all of them.  Calls that may
+ *                run at the same time need workspaces of their own.
  *   dx may be dskip itself; no other output may overlap an input.
  *   rows == 0 writes zeros to dgamma and dbeta; cols == 0 enqueues nothing.
  */

@@ -768,6 +768,18 @@ inline int norm_tiles(int64_t rows, int64_t cols) {
   return (int)(t < most ? t : most);
 }
 
+// Bytes of both gradients' partial sums, from bounds of norm_tiles that grow with the rows and the columns (it does
+// not itself: 512 rows of sums for 2047 rows of 1024 columns, 256 for 4096): the workspace of the longest and widest
+// call serves every smaller one.  Up to 2048 chunks norm_tiles is at most min(rows, two a CU), past them
+// min(ceil(rows / 32), one a CU), taken as no fewer bytes than 2048 chunks have.
+inline size_t norm_workspace(int64_t rows, int64_t cols) {
+  constexpr int64_t kHeld = 2048 * kChunk;
+  const int64_t cus = device_cu_count();
+  const int64_t held = (cols < kHeld ? cols : kHeld) * (rows < 2 * cus ? rows : 2 * cus);
+  const int64_t tiles = (rows + 31) / 32, wide = cols > kHeld ? cols * (tiles < cus ? tiles : cus) : 0;
+  return (size_t)2 * sizeof(float) * (size_t)(held > wide ? held : wide);
+}
+
 // f(NT) for a row's threads, false where no register kernel takes the row
 template <class F>
 bool with_threads(int nt, F f) {
@@ -933,7 +945,7 @@ extern "C" te_status te_norm_forward(te_norm_kind kind, const void* x, te_dtype 
 extern "C" size_t te_norm_backward_workspace_size(int64_t rows, int64_t cols) {
   constexpr int64_t kMost = ((int64_t)1 << 31) - 65536;
   if (rows <= 0 || cols <= 0 || rows > kMost || cols > kMost) return 0;
-  return (size_t)2 * norm_tiles(rows, cols) * (size_t)cols * sizeof(float);
+  return norm_workspace(rows, cols);
 }
 
 extern "C" te_status te_norm_backward(te_norm_kind kind, const void* dy, const void* x, const void* dskip,

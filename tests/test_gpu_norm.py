@@ -319,3 +319,22 @@ def test_more_rows_than_one_launch_holds():
     # dbeta: exact to the paths' rounding (at most 100 + rows / 32 additions, here far fewer: rows / 16384 + 200)
     bound = (rows / 16384 + 200) * U * x.double().abs().sum(0)
     assert ((db.double() - x.double().sum(0)).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("cols", [130, 1024, 2048])
+def test_backward_batches_share_the_workspace_of_the_longest(cols):
+    """Shorter last batches of a program that allocated once, for its longest: same bits as with a workspace of their
+    own, and nothing written behind what is asked for."""
+    m = te()
+    longest = 4096
+    size = m.te_norm_backward_workspace_size(longest, cols)
+    raw = torch.full((size + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+    gamma, _ = weights(9, cols, torch.float32)
+    for rows in (longest, 2047, 1023, 511, 300, 1):
+        x, dy = make(rows, rows, cols, torch.bfloat16), make(rows + 1, rows, cols, torch.bfloat16, 0.1)
+        mean, rstd = stats(x, "layer")
+        want = backward(dy, x, gamma, mean, rstd, "layer")
+        dx, dg, db = torch.empty_like(x), torch.empty_like(gamma), torch.empty_like(gamma)
+        m.te_norm_backward("layer", dy, x, gamma, mean, rstd, dx, dg, db, workspace=raw[:size])
+        assert torch.equal(dx, want[0]) and torch.equal(dg, want[1]) and torch.equal(db, want[2]), rows
+        assert (raw[size:] == 0xA5).all()

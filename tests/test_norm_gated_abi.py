@@ -165,3 +165,28 @@ def test_wrappers_refuse_wrong_tensors():
         te.te_mxfp8_dgated_gemm(None, s, "e4m3", b, bs, "e4m3", None, None)
     with pytest.raises(ValueError, match="m_splits"):
         te.te_mxfp8_grouped_gated_gemm(None, q, s, "e4m3", b, bs, "e4m3", 16, None)
+
+
+@pytest.mark.parametrize("cols", [1, 16, 130, 1024, 2048, 2056, 5120, 5128, 8192, 8200, 16384, 16392, 70001])
+def test_norm_backward_workspace_of_a_batch_serves_smaller_ones(cols):
+    """A program that sizes its workspace for its longest batch has enough for every shorter one."""
+    rows = sorted({r + d for e in range(21) for r in (1 << e,) for d in (-1, 0, 1)} - {0})
+    sizes = [te.te_norm_backward_workspace_size(r, cols) for r in rows]
+    assert sizes == sorted(sizes)
+    assert bwd(rows=rows[5], cols=cols, ws_bytes=sizes[5] - 1) == te.TE_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("rows", [1, 37, 255, 511, 1023, 2047, 4096, 16384, 1 << 20])
+def test_norm_backward_workspace_of_the_widest_norm_serves_narrower_ones(rows):
+    cols = sorted({8 * nt + d for nt in (16, 32, 64, 128, 192, 256, 512, 640, 768, 1024, 2048, 4096)
+                   for d in (-8, -1, 0, 1, 8)})
+    sizes = [te.te_norm_backward_workspace_size(rows, c) for c in cols]
+    assert sizes == sorted(sizes)
+
+
+def test_norm_backward_workspace_holds_the_partial_sums_of_every_batch():
+    """Never less than one row of both gradients' sums, and bounded: two for each CU, or those of 16384 columns."""
+    for rows in (1, 100, 5000, 1 << 20):
+        for cols in (1, 77, 4096, 16384, 16385, 70001):
+            size = te.te_norm_backward_workspace_size(rows, cols)
+            assert 8 * cols <= size <= 8 * 512 * max(cols, 16384)
