@@ -205,3 +205,82 @@ def test_the_same_call_gives_the_same_bits(M, N, K):
         out += [g, ga, gd]
         assert first is None or all(torch.equal(x, y) for x, y in zip(first, out))
         first = out
+
+
+# ---------------------------------------------------------------- NaN operands
+
+NAN_CODE = 0x7F  # E4M3
+
+
+def nan_at(t):
+    return torch.isnan(t.view(torch.bfloat16))
+
+
+# few rows (8 and 4 waves, a run that ends ragged), the small tiles, the 8-wave tile, the 4-wave tile
+@pytest.mark.parametrize("M,N,K", [(1, 32, 128), (7, 64, 640), (20, 8224, 128), (50, 96, 4224), (70, 96, 384),
+                                   (400, 1056, 2304), (1300, 4128, 384), (2100, 2336, 4096)])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_nan_operands_stay_in_their_rows_and_columns(M, N, K, act):
+    m = te()
+    a, b = quantized(31, M, K), quantized(32, 2 * N, K, sigma=0.05)
+    size = m.te_mxfp8_gated_gemm_workspace_size(M, N, K)
+    r, gate, up = M - 1, 5, N - 2
+
+    def run(qa, qb):
+        ws = torch.empty(size, dtype=torch.uint8, device="cuda") if size else None
+        d, aux = filled((M, N)), filled((M, 2 * N))
+        q, s = (torch.empty((M, n), dtype=torch.uint8, device="cuda") for n in (N, N // 32))
+        m.te_mxfp8_gated_gemm(qa, a[1], "e4m3", qb, b[1], "e4m3", d, act, aux=aux, workspace=ws)
+        m.te_mxfp8_gated_gemm(qa, a[1], "e4m3", qb, b[1], "e4m3", q, act, d_scale=s, d_fmt="e4m3", workspace=ws)
+        want = m.mxfp8_quantize(d, "e4m3", "row")
+        if not 32 < M <= 64:  # (the 4-wave few-row form adds in another order)
+            assert torch.equal(q, want[0]) and torch.equal(s, want[1])
+        pre = torch.ones((M, 2 * N), dtype=torch.bfloat16, device="cuda")
+        dd = filled((M, 2 * N))
+        m.te_mxfp8_dgated_gemm(qa, a[1], "e4m3", qb[:N], b[1][:N], "e4m3", pre, dd, act)
+        return d, aux, dd
+
+    clean = run(a[0], b[0])
+    qa, qb = a[0].clone(), b[0].clone()
+    qa[r, K - 3] = NAN_CODE
+    qb[gate, 2] = qb[N + up, K - 1] = NAN_CODE
+    got = run(qa, qb)
+    bad = [torch.zeros(t.shape, dtype=torch.bool, device="cuda") for t in got]
+    for t in bad:
+        t[r] = True
+    bad[0][:, [gate, up]] = True
+    bad[1][:, [gate, N + up]] = True
+    bad[2][:, [gate, N + gate]] = True
+    for t, c, where in zip(got, clean, bad):
+        assert torch.equal(nan_at(t), where)
+        assert torch.equal(t[~where], c[~where])
+
+
+def test_nan_operands_stay_in_their_groups():
+    m = te()
+    counts, N, K = [130, 0, 1, 300, 70], 1040, 384
+    total, G = sum(counts), len(counts)
+    a, b = quantized(33, total, K), quantized(34, G * 2 * N, K, sigma=0.05)
+    splits = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    pre = torch.ones((total, 2 * N), dtype=torch.bfloat16, device="cuda")
+
+    def run(qa, qb):
+        d, aux, dd = filled((total, N)), filled((total, 2 * N)), filled((total, 2 * N))
+        m.te_mxfp8_grouped_gated_gemm(splits, qa, a[1], "e4m3", qb, b[1], "e4m3", N, d, aux=aux)
+        m.te_mxfp8_grouped_dgated_gemm(splits, qa, a[1], "e4m3", qb[:G * N], b[1][:G * N], "e4m3", N, pre, dd)
+        return d, aux, dd
+
+    clean = run(a[0], b[0])
+    qa, qb = a[0].clone(), b[0].clone()
+    qa[130] = NAN_CODE                    # group 2's only row
+    qb[2 * N:4 * N] = NAN_CODE            # the weights of group 1, which has no rows (backward: those of 2 and 3)
+    qb[3 * 2 * N + 7] = NAN_CODE          # forward: column 7 of group 3's gate
+    got = run(qa, qb)
+    bad = [torch.zeros(t.shape, dtype=torch.bool, device="cuda") for t in got]
+    for t in bad:
+        t[130] = True
+    bad[0][131:431, 7] = bad[1][131:431, 7] = True
+    bad[2][130:431] = True
+    for t, c, where in zip(got, clean, bad):
+        assert torch.equal(nan_at(t), where)
+        assert torch.equal(t[~where], c[~where])

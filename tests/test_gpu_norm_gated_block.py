@@ -275,3 +275,14 @@ def test_gpu_refusals():
         m.mxfp8_gated_gemm(a, sa, "e5m2", b, sb, "e5m2")
     with pytest.raises(m.TemxError, match="TE_ERR_SHAPE"):
         m.mxfp8_gated_gemm(a, sa, "e4m3", b, sb, "e4m3", out_fmt="e4m3")  # N = 48
+
+
+def test_streams_given_as_handles():
+    b = Block(128 * 32, 256, 384)  # (the weight gradient contracts over the tokens: whole 128s)
+    want = b.run()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for handle in (side.cuda_stream, torch.cuda.current_stream().cuda_stream, 0):
+        got = b.run(stream=handle)
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[n], want[n]) for n in want), handle
