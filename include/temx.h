@@ -508,7 +508,8 @@ te_status te_norm_backward(te_norm_kind kind, const void* dy, const void* x, con
  *   K <= 2^23, N <= 2^22, M < 2^31 - 256, 2N K / 32 < 2^31 - 4096.
  *   M == 0 or N == 0 enqueues nothing; K == 0 gives P = bias.
  *   workspace: optional, as te_mxfp8_gemm's (te_mxfp8_gated_gemm_workspace_size
- *   bytes enable the faster path; same results without).
+ *   bytes enable the 4-wave kernel, faster on most large shapes and a few
+ *   percent slower on some; same results without).
  */
 size_t te_mxfp8_gated_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
 te_status te_mxfp8_gated_gemm(const uint8_t* a, const uint8_t* a_scale, te_dtype a_fmt, const uint8_t* b,

@@ -14,15 +14,19 @@
 // [M, N]), and from the saved pre-activations aux = [gate | up] ([M, 2N])
 //   D[m, n] = acc up act'(gate),  D[m, N + n] = acc act(gate).
 //
-// Bounds and times on MI355X (M x N x K):
-//   forward 8192 x 14336 x 4096 to MXFP8: the main loop's MFMA rate; 764 us,
-//     2.52 PFLOP/s (a plain GEMM of that size to bf16: 757 us)
+// Bounds and times on MI355X (M x N x K), us a call with its scale
+// rearrangement, in a stream of calls whose inputs are not in the caches (a
+// profiler's trace, which keeps dispatches apart, gives up to 9% more):
+//   forward 8192 x 14336 x 4096 to MXFP8: the main loop's MFMA rate; 753,
+//     2.55 PFLOP/s (a plain GEMM of both projections to bf16: 739)
 //   forward 4096 x 4096 x 1024 with bias and aux: two rounds of tiles of 8 K
-//     steps, and the 100 MB they write; 46-49 us (a plain GEMM, 67 MB: 43 us)
-//   backward 4096 x 4096 x 1024: 143 MB of aux, gradients and operands; 35 us
-//   backward 4096 x 14336 x 4096: 250 us, of them 175 the main loop (1.92
-//     PFLOP/s over all): every CU's tile ends at the same time, so the 470 MB of
-//     aux and gradients move in bursts that no MFMA covers
+//     steps, and the 100 MB they write; 53 (48 with inputs in the last-level
+//     cache; without bias and aux 42, a plain GEMM, 67 MB, 43)
+//   backward 4096 x 4096 x 1024: 143 MB of aux, gradients and operands; 41 (35
+//     with inputs in the last-level cache)
+//   backward 4096 x 14336 x 4096: 248, of them 175 the main loop (1.94 PFLOP/s
+//     over all): every CU's tile ends at the same time, so the 470 MB of aux
+//     and gradients move in bursts that no MFMA covers
 #pragma once
 
 #include "gemm_core.h"

@@ -46,8 +46,11 @@ size_t gated_workspace(int64_t M, int64_t cols, int64_t K, int64_t N) {
 }
 
 // The few-row kernel instead of a tile: up to 64 rows; from 33 only where 128-row tiles would leave a quarter of the
-// CUs idle (N = 14336, K = 4096, 64 rows: 54 us against 35 with tiles; N = 8192, K = 8192: 55 against 57; N = 4096,
-// K = 4096: 16 against 29).
+// CUs idle (N = 14336, K = 4096, 64 rows: 54 us against 37 with tiles; N = 8192, K = 8192: 56 against 57; N = 4096,
+// K = 4096: 17 against 29).  Forward only: a backward of few rows takes the tiles, (N + 127) / 128 workgroups that each
+// walk all of K, a third of the CUs or less at these sizes (one and 128 rows, us, and one row's weights at a copy's
+// rate: N = 14336, K = 4096 28, 36 and 12; N = K = 8192 47, 61 and 14; N = K = 4096 27, 34 and 3; N = 2048, K = 8192
+// 46, 59 and 3).  Gradients are taken of batches, so it has no kernel of its own.
 bool few_rows(int64_t M, int64_t N) {
   return M <= 32 || (M <= kFewRows && 4 * ((2 * N + 127) / 128) < 3 * (int64_t)device_cu_count());
 }
@@ -154,8 +157,9 @@ te_status grouped_gated(GatedParams p, te_dtype a_fmt, te_dtype b_fmt, hipStream
   // The splits stay on the device.  Groups of at most a small tile's rows on average take that tile: the weights bound
   // them, and its grid is 4 times as fine (big and small tile, us, forward / backward: N = K = 2048, 8 rows over 64
   // groups 26 / 29 and 20 / 22, 16 groups of 40 rows 35 / 25 and 33 / 20, 16 of 200 rows 43 / 46 and 55 / 38; 32 groups
-  // of 64 rows, N = 1536, K = 4096, 123 / 70 and 113 / 71).  Else by the big-tile count, estimated from the total rows
-  // and one ragged tail per group.
+  // of 64 rows, N = 1536, K = 4096, 123 / 70 and 113 / 71).  One rule for both directions: it is the forward's, and the
+  // backward of 16 groups of 200 rows takes the tile that is 8 us slower there.  Else by the big-tile count, estimated
+  // from the total rows and one ragged tail per group.
   if (p.M <= 128 * (int64_t)p.groups || use_small_tile((p.M / 256 + p.groups) * ((cols + 255) / 256)))
     return launch_grouped_gated<Small, BWD>(p, a_fmt, b_fmt, 2 * grid, stream);
   return launch_grouped_gated<Big, BWD>(p, a_fmt, b_fmt, grid, stream);

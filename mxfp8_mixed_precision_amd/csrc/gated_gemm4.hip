@@ -34,10 +34,10 @@ __global__ __launch_bounds__(256) void gated_scale_blocks_kernel(const uint8_t* 
 
 // The 4-wave big tile, persistent over its tiles as mx_gemm4_kernel is: the next tile's first copies are issued
 // before a tile's epilogue, which stages in stage 1.  p.a_scale / p.b_scale are the rearranged copies.
-// Taken where four_wave_mx takes it for a plain GEMM of as many tiles.  4-wave and 8-wave, us, on inputs that are not
-// in the caches: forward to MXFP8 8192 x 14336 x 4096 731 and 788; forward with aux 4096 x 4096 x 4096 127 and 130,
-// 1024 x 8192 x 4096 69 and 65; backward 4096 x 14336 x 4096 247 and 284, 4096 x 4096 x 4096 70 and 80, 8192 x 8192 x
-// 2048 219 and 210.
+// Taken where four_wave_mx takes it for a plain GEMM of as many tiles, which loses 4-6% on two of these.  4-wave and
+// 8-wave, us, in turn, the best of four rounds on inputs that are not in the caches: forward to MXFP8 8192 x 14336 x
+// 4096 731 and 788; forward with aux 4096 x 4096 x 4096 127 and 130, 1024 x 8192 x 4096 69 and 65; backward 4096 x
+// 14336 x 4096 247 and 284, 4096 x 4096 x 4096 70 and 80, 8192 x 8192 x 2048 219 and 210.
 template <int FA, int FB, bool BWD>
 __global__ __launch_bounds__(Big4::kThreads, 1) void gated_gemm4_kernel(GatedParams p) {
   using LY = Big4;

@@ -10,8 +10,10 @@
 // LDS and are added in wave order (deterministic); bias, activation, product
 // and the MXFP8 encode follow.  All reads go through buffer resources: rows
 // past M and K steps past the end read zeros.
-// Measured on MI355X, one row, N = 14336, K = 4096: 25.3 us, 121 MB of weights
-// and scales at 4.8 TB/s (a large copy: 5.1).
+// Measured on MI355X, one row, N = 14336, K = 4096: 25.5 us, 121 MB of weights
+// and scales at 4.8 TB/s (a large copy: 5.1).  Every workgroup reads all of A,
+// twice its weights' bytes at 64 rows: 64 rows of N = K = 4096 take 17 us, of
+// N = K = 8192 56 us, where the weights alone take 7 and 27.
 #include "gated_core.h"
 
 namespace temx {
@@ -153,9 +155,10 @@ te_status launch(const GatedParams& p, te_dtype fa, te_dtype fb, hipStream_t str
 }  // namespace
 
 // 8 waves and 16 columns a workgroup: as many CUs as possible read weights (one CU takes in ~26 bytes a ns whatever
-// its waves; K = 8192, N = 2048, one row: 12 us with 16 columns, 21.5 with 32).  32 columns where MXFP8 output needs
-// its 32-blocks, and for 17 to 32 rows of wide layers, which read the rows' operands half as often (N = 14336,
-// K = 4096, 32 rows: 40 -> 35 us; N = 8192, K = 8192: 42 -> 39, N = 4096, K = 4096: 12.8 -> 18).
+// its waves; K = 8192, N = 2048, one row: 12 us with 16 columns, 21.8 with 32).  32 columns where MXFP8 output needs
+// its 32-blocks (64 workgroups for that row to MXFP8, 21.8 us), and for 17 to 32 rows of wide layers, which read the
+// rows' operands half as often (N = 14336, K = 4096, 32 rows: 40 -> 35 us; N = 8192, K = 8192: 42 -> 41, N = 4096,
+// K = 4096: 13 -> 18).
 te_status launch_gated_rows(const GatedParams& p, te_dtype fa, te_dtype fb, hipStream_t stream) {
   if (p.out == TE_BF16) {
     if (p.M <= 16) return launch<8, 1, 1>(p, fa, fb, stream);
