@@ -15,7 +15,11 @@
  *   - a single-launch grouped (MoE) variant over ragged expert row counts;
  *   - layer norm / RMS norm, forward and backward, and the gated
  *     feed-forward GEMMs (both projections, activation and product in one
- *     kernel), forward and backward, dense and grouped.
+ *     kernel), forward and backward, dense and grouped;
+ *   - around the grouped GEMMs: the router, tokens sorted by expert and back
+ *     with the router's weights, and their gradients;
+ *   - GEMMs of few rows with 4-bit weights and group scales, plain and gated,
+ *     dense and grouped.
  *
  * Sources, cited by page title and section:
  *   [ROCm-TE]  "Transformer Engine On ROCm and AMDGPU" (ROCm/TransformerEngine
@@ -109,6 +113,12 @@ typedef enum { TE_NORM_LAYER = 0, TE_NORM_RMS = 1 } te_norm_kind;
 
 /* The gate activation of a gated feed-forward block (TE_ACT_GELU: the tanh form). */
 typedef enum { TE_ACT_SILU = 0, TE_ACT_GELU = 1 } te_activation;
+
+/* The scores of a router: softmax over the experts, or each expert's sigmoid. */
+typedef enum { TE_SCORE_SOFTMAX = 0, TE_SCORE_SIGMOID = 1 } te_score;
+
+/* Codes of 4-bit weights: integers 0 .. 15 with a zero point, or the 4-bit MX element format. */
+typedef enum { TE_W4_INT4 = 0, TE_W4_E2M1 = 1 } te_w4_format;
 
 /* Human-readable name of a status code (static storage). */
 const char* te_status_str(te_status status);
@@ -558,6 +568,170 @@ te_status te_mxfp8_grouped_dgated_gemm(int32_t num_groups, const int32_t* m_spli
                                        const uint8_t* a_scale, te_dtype a_fmt, const uint8_t* b,
                                        const uint8_t* b_scale, te_dtype b_fmt, int64_t N, int64_t K,
                                        te_activation act, const uint16_t* aux, uint16_t* d, hipStream_t stream);
+
+/*
+ * The router of a mixture-of-experts block: each token's experts and weights
+ * from its logits l (an expert whose logit is -inf is masked for that token).
+ *   s_e  = softmax(l)_e over the experts that are not masked
+ *          (TE_SCORE_SOFTMAX), or 1 / (1 + exp(-l_e)) (TE_SCORE_SIGMOID)
+ *   experts[t, :] = the topk experts of the largest s_e + bias[e] (without a
+ *          bias: of the largest logits) in falling order, equal ones in rising
+ *          order of e; -1 where no unmasked expert is left.  Sums with a bias
+ *          are compared in 64 bits.
+ *   weights[t, k] = scale * s_{experts[t, k]}, divided with normalize = 1 by
+ *          the sum of the token's chosen s; 0 where experts[t, k] is -1
+ *   logits   dtype [tokens, num_experts]: TE_BF16, TE_FP16 or TE_FP32;
+ *            16-byte aligned
+ *   bias     float [num_experts], or NULL: enters the choice alone (load
+ *            balancing); -inf masks the expert in the choice for every token
+ *   normalize 0 or 1;  scale finite
+ *   experts  int32 [tokens, topk], weights float [tokens, topk]
+ *   num_experts 1 .. 1024, topk 1 .. min(num_experts, 64), tokens >= 0,
+ *   tokens * topk < 2^31 - 65536.
+ * An expert whose logit (or logit's sum with the bias) is NaN is not chosen; a
+ * NaN logit makes the softmax shares (normalize = 0) of its token NaN.
+ */
+te_status te_moe_route(te_score score, const void* logits, te_dtype dtype, int64_t tokens, int32_t num_experts,
+                       int32_t topk, const float* bias, int normalize, float scale, int32_t* experts, float* weights,
+                       hipStream_t stream);
+
+/*
+ * The backward pass of te_moe_route: the gradient of the logits from the
+ * weights', for the experts that the forward chose (the choice itself has no
+ * gradient, nor has the bias).  Scores are computed again from the logits.
+ *   experts  int32 [tokens, topk]: slots that are not in [0, num_experts) are
+ *            left out (their weight was 0)
+ *   dweights float [tokens, topk]
+ *   dlogits  dtype [tokens, num_experts], written whole; 16-byte aligned
+ *   The rest as te_moe_route.  A token's experts are distinct (the gradients
+ *   of two slots that name one expert are added).
+ */
+te_status te_moe_route_backward(te_score score, const void* logits, te_dtype dtype, int64_t tokens,
+                                int32_t num_experts, int32_t topk, int normalize, float scale, const int32_t* experts,
+                                const float* dweights, void* dlogits, hipStream_t stream);
+
+/*
+ * The sort of a batch's slots (a slot = one expert of one token, slot
+ * t * topk + k) by expert, stable: the rows of the grouped GEMMs.
+ *   experts   int32 [slots]; slots that are not in [0, num_experts) get no row
+ *   m_splits  int32 [num_experts]: rows of each expert, what the grouped GEMMs
+ *             take
+ *   row_of    int32 [slots]: each slot's row, -1 where it has none
+ *   slot_of   int32 [slots]: each row's slot, -1 behind the last row
+ *   slots 0 .. 2^31 - 65536, num_experts 1 .. 1024; all pointers 4-byte aligned
+ *   workspace device scratch of at least te_moe_sort_workspace_size(slots,
+ *             num_experts) bytes, 4-byte aligned (NULL where that is 0).  Calls
+ *             that may run at the same time need workspaces of their own.
+ * slots == 0 writes zeros to m_splits.
+ */
+size_t te_moe_sort_workspace_size(int64_t slots, int32_t num_experts);
+te_status te_moe_sort(const int32_t* experts, int64_t slots, int32_t num_experts, int32_t* m_splits, int32_t* row_of,
+                      int32_t* slot_of, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Tokens to their experts' rows:  y[row_of[t, k], :] = x[t, :].
+ *   x, y     dtype [tokens, cols] and [total_rows, cols]: TE_BF16, TE_FP16 or
+ *            TE_FP32, y NULL where q is given
+ *   row_of   int32 [tokens, topk] as te_moe_sort gives it; slots without a row
+ *            in [0, total_rows) are left out, rows of no slot stay as they were.
+ *            Two slots of one row: unspecified contents of that row.
+ *   q, q_scale both or neither: the rows as the grouped GEMMs' MXFP8 operand
+ *            (q_fmt TE_E4M3 or TE_E5M2), each exactly as te_mxfp8_quantize
+ *            (TE_ROWWISE) gives it; needs dtype TE_BF16 and cols % 32 == 0
+ *   topk 1 .. 64; tokens * topk, total_rows, cols < 2^31 - 65536.  Tensors are
+ *   16-byte aligned (row_of 4), inputs and outputs do not overlap.
+ * Its gradient is te_moe_combine without weights.
+ */
+te_status te_moe_dispatch(const void* x, te_dtype dtype, int64_t tokens, int64_t cols, const int32_t* row_of,
+                          int32_t topk, int64_t total_rows, void* y, uint8_t* q, uint8_t* q_scale, te_dtype q_fmt,
+                          hipStream_t stream);
+
+/*
+ * The experts' rows back to their tokens:
+ *   y[t, :] = sum_k weights[t, k] * rows[row_of[t, k], :]
+ * added up in fp32 in the order of k (slots without a row are left out), rounded
+ * once.
+ *   rows, y  dtype [total_rows, cols] and [tokens, cols]
+ *   weights  float [tokens, topk], or NULL: all 1 (the gradient of
+ *            te_moe_dispatch: rows = dy, y = dx)
+ *   The rest as te_moe_dispatch.
+ */
+te_status te_moe_combine(const void* rows, te_dtype dtype, int64_t total_rows, int64_t cols, const int32_t* row_of,
+                         const float* weights, int64_t tokens, int32_t topk, void* y, hipStream_t stream);
+
+/*
+ * The backward pass of te_moe_combine with weights:
+ *   drows[row_of[t, k], :] = weights[t, k] * dy[t, :]
+ *   dweights[t, k] = sum_c dy[t, c] * rows[row_of[t, k], c]   (fp32, in a fixed
+ *                    order; 0 for a slot without a row)
+ *   dy       dtype [tokens, cols]; rows dtype [total_rows, cols]: what the
+ *            forward combined
+ *   drows    dtype [total_rows, cols], NULL where q is given; rows of no slot
+ *            stay as they were
+ *   q, q_scale both or neither: drows as MXFP8 operand, as te_moe_dispatch's
+ *   dweights float [tokens, topk]
+ *   The rest as te_moe_dispatch.
+ */
+te_status te_moe_combine_backward(const void* dy, const void* rows, te_dtype dtype, int64_t tokens, int64_t cols,
+                                  const int32_t* row_of, const float* weights, int32_t topk, int64_t total_rows,
+                                  void* drows, uint8_t* q, uint8_t* q_scale, te_dtype q_fmt, float* dweights,
+                                  hipStream_t stream);
+
+/*
+ * GEMM with 4-bit weights and group scales, "TN", made for few rows (decoding):
+ *   P[m, n] = sum_g w_scale[n, g] * sum_{k in group g} x[m, k] * (q[n, k] - z[n, g])
+ *             + bias[n]
+ * with fp32 products and sums, D = P rounded once.
+ *   x        dtype [M, K]: TE_BF16 or TE_FP16
+ *   w        uint8 [N, K/2]: q[n, 2j] in the low half of byte j, q[n, 2j + 1]
+ *            in the high half
+ *   w_fmt    TE_W4_INT4: q = 0 .. 15, z = w_zero[n, g], or 8 where w_zero is
+ *            NULL.  TE_W4_E2M1: q = the value of the code (+-0, 0.5, 1, 1.5, 2,
+ *            3, 4, 6), z = 0 and w_zero NULL.
+ *   group_size  K elements of one scale: a multiple of 32 that divides K
+ *   w_scale  [N, K/group_size] of scale_dtype dtype, TE_FP32 or TE_E8M0 (code
+ *            255 is NaN)
+ *   w_zero   uint8 [N, K/group_size], or NULL
+ *   d        [M, N], d_dtype dtype or TE_FP32
+ *   bias     dtype [N], or NULL
+ *   Shapes: any M, N >= 0 (any M is right; from about 64 rows up a GEMM on
+ *   quantized activations is the faster one); M, 2N, K < 2^31 - 65536.  M == 0
+ *   or N == 0 enqueues nothing; K == 0 gives P = bias.
+ *   x, w and d are 16-byte aligned; scales and bias to their type.
+ *   A non-finite value of x affects its own row of D only; with TE_W4_INT4 an
+ *   infinite one gives NaN where the formula gives an infinity.
+ */
+te_status te_w4_gemm(const void* x, te_dtype dtype, const uint8_t* w, te_w4_format w_fmt, const void* w_scale,
+                     te_dtype scale_dtype, const uint8_t* w_zero, int32_t group_size, int64_t M, int64_t N, int64_t K,
+                     void* d, te_dtype d_dtype, const void* bias, hipStream_t stream);
+
+/*
+ * The gated form: P [M, 2N] as above with w [2N, K/2] (the N gate rows first;
+ * scales, zero points and bias likewise),
+ *   D[m, n] = act(P[m, n]) * P[m, N + n],   fp32 up to one rounding of D.
+ */
+te_status te_w4_gated_gemm(const void* x, te_dtype dtype, const uint8_t* w, te_w4_format w_fmt, const void* w_scale,
+                           te_dtype scale_dtype, const uint8_t* w_zero, int32_t group_size, int64_t M, int64_t N,
+                           int64_t K, te_activation act, void* d, te_dtype d_dtype, const void* bias,
+                           hipStream_t stream);
+
+/*
+ * The two above over ragged groups of rows (experts) in one launch: group g owns
+ * rows [off_g, off_g + m_splits[g]) of x and D, and its own weights, scales, zero
+ * points and bias (stacked: w uint8 [G * N, K/2], gated [G * 2N, K/2]; bias
+ * [G, N] or [G, 2N]).  m_splits and num_groups as te_mxfp8_grouped_gated_gemm:
+ * rows behind the last group stay as they were, bad splits cannot read or write
+ * outside the tensors.  N, K > 0.
+ */
+te_status te_w4_grouped_gemm(int32_t num_groups, const int32_t* m_splits, int64_t total_m, const void* x,
+                             te_dtype dtype, const uint8_t* w, te_w4_format w_fmt, const void* w_scale,
+                             te_dtype scale_dtype, const uint8_t* w_zero, int32_t group_size, int64_t N, int64_t K,
+                             void* d, te_dtype d_dtype, const void* bias, hipStream_t stream);
+te_status te_w4_grouped_gated_gemm(int32_t num_groups, const int32_t* m_splits, int64_t total_m, const void* x,
+                                   te_dtype dtype, const uint8_t* w, te_w4_format w_fmt, const void* w_scale,
+                                   te_dtype scale_dtype, const uint8_t* w_zero, int32_t group_size, int64_t N,
+                                   int64_t K, te_activation act, void* d, te_dtype d_dtype, const void* bias,
+                                   hipStream_t stream);
 
 #ifdef __cplusplus
 }

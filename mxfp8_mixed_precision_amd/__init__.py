@@ -33,6 +33,10 @@ TE_NORM_LAYER, TE_NORM_RMS = 0, 1
 NORM_KINDS = {"layer": TE_NORM_LAYER, "rms": TE_NORM_RMS}
 TE_ACT_SILU, TE_ACT_GELU = 0, 1
 ACTIVATIONS = {"silu": TE_ACT_SILU, "gelu": TE_ACT_GELU}
+TE_SCORE_SOFTMAX, TE_SCORE_SIGMOID = 0, 1
+SCORES = {"softmax": TE_SCORE_SOFTMAX, "sigmoid": TE_SCORE_SIGMOID}
+TE_W4_INT4, TE_W4_E2M1 = 0, 1
+W4_FORMATS = {"int4": TE_W4_INT4, "e2m1": TE_W4_E2M1}
 BLOCK_SCALINGS = {"e8m0": TE_BLOCK_SCALES_E8M0, "fp32": TE_BLOCK_SCALES_FP32}
 
 FORMATS = {"e4m3": TE_E4M3, "e5m2": TE_E5M2}
@@ -83,6 +87,25 @@ _SIGS = {
                                                    _i64, _i64, ctypes.c_int, _vp, _vp, _vp, _vp]),
     "te_mxfp8_grouped_dgated_gemm": (ctypes.c_int, [_i32, _vp, _i64, _vp, _vp, ctypes.c_int, _vp, _vp, ctypes.c_int,
                                                     _i64, _i64, ctypes.c_int, _vp, _vp, _vp]),
+    "te_moe_route": (ctypes.c_int, [ctypes.c_int, _vp, ctypes.c_int, _i64, _i32, _i32, _vp, ctypes.c_int, ctypes.c_float,
+                                    _vp, _vp, _vp]),
+    "te_moe_route_backward": (ctypes.c_int, [ctypes.c_int, _vp, ctypes.c_int, _i64, _i32, _i32, ctypes.c_int,
+                                             ctypes.c_float, _vp, _vp, _vp, _vp]),
+    "te_moe_sort_workspace_size": (_sz, [_i64, _i32]),
+    "te_moe_sort": (ctypes.c_int, [_vp, _i64, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "te_moe_dispatch": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _vp, _i32, _i64, _vp, _vp, _vp, ctypes.c_int, _vp]),
+    "te_moe_combine": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _vp, _vp, _i64, _i32, _vp, _vp]),
+    "te_moe_combine_backward": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _vp, _vp,
+                                               ctypes.c_int, _vp, _vp]),
+    "te_w4_gemm": (ctypes.c_int, [_vp, ctypes.c_int, _vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _i32, _i64, _i64, _i64,
+                                  _vp, ctypes.c_int, _vp, _vp]),
+    "te_w4_gated_gemm": (ctypes.c_int, [_vp, ctypes.c_int, _vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _i32, _i64, _i64,
+                                        _i64, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp]),
+    "te_w4_grouped_gemm": (ctypes.c_int, [_i32, _vp, _i64, _vp, ctypes.c_int, _vp, ctypes.c_int, _vp, ctypes.c_int, _vp,
+                                          _i32, _i64, _i64, _vp, ctypes.c_int, _vp, _vp]),
+    "te_w4_grouped_gated_gemm": (ctypes.c_int, [_i32, _vp, _i64, _vp, ctypes.c_int, _vp, ctypes.c_int, _vp,
+                                                ctypes.c_int, _vp, _i32, _i64, _i64, ctypes.c_int, _vp, ctypes.c_int,
+                                                _vp, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -599,6 +622,174 @@ def te_mxfp8_grouped_dgated_gemm(m_splits, a, a_scale, a_fmt, b, b_scale, b_fmt,
         _addr(aux, "aux", (M, 2 * n), _B16, i), _addr(d, "d", (M, 2 * n), _B16, i)), i, stream)
 
 
+# ------------------------------------- the router, and tokens to their experts' rows and back
+
+def _score(score) -> int:
+    return SCORES[score] if isinstance(score, str) else int(score)
+
+
+def _route_args(score, logits, experts):
+    """(device index, score, logits' address and dtype, tokens, experts in all, topk, experts' address)"""
+    index = _index_of(logits, "logits")
+    _require(logits.dtype in _NORM_DTYPES, f"logits: expected {_FLOATS}, got {logits.dtype}")
+    _require(experts is not None and experts.dim() == 2, "experts: expected a 2-D int32 tensor")
+    tokens, n = logits.shape
+    topk = experts.shape[1]
+    return (index, _score(score), _addr(logits, "logits", (tokens, n), logits.dtype, index), _NORM_DTYPES[logits.dtype],
+            tokens, n, topk, _addr(experts, "experts", (tokens, topk), "int32", index))
+
+
+def te_moe_route(score, logits, experts, weights, bias=None, normalize=True, scale=1.0, stream=None) -> None:
+    """experts int32 [tokens, topk] and weights float32 [tokens, topk] are written."""
+    i, score, logits_at, dt, tokens, n, topk, experts_at = _route_args(score, logits, experts)
+    _run("te_moe_route", (
+        score, logits_at, dt, tokens, n, topk, _opt(bias, "bias", (n,), "float32", i), int(bool(normalize)), scale,
+        experts_at, _addr(weights, "weights", (tokens, topk), "float32", i)), i, stream)
+
+
+def te_moe_route_backward(score, logits, experts, dweights, dlogits, normalize=True, scale=1.0, stream=None) -> None:
+    i, score, logits_at, dt, tokens, n, topk, experts_at = _route_args(score, logits, experts)
+    _run("te_moe_route_backward", (
+        score, logits_at, dt, tokens, n, topk, int(bool(normalize)), scale, experts_at,
+        _addr(dweights, "dweights", (tokens, topk), "float32", i),
+        _addr(dlogits, "dlogits", (tokens, n), logits.dtype, i)), i, stream)
+
+
+def te_moe_sort_workspace_size(slots: int, num_experts: int) -> int:
+    return int(_lib.te_moe_sort_workspace_size(int(slots), int(num_experts)))
+
+
+def te_moe_sort(experts, m_splits, row_of, slot_of, workspace=None, stream=None) -> None:
+    """experts int32 of any shape (its slots in row-major order); row_of has its shape, slot_of its number of slots."""
+    _require(isinstance(experts, torch.Tensor), "experts is required")
+    i, shape, slots = experts.get_device(), experts.shape, experts.numel()
+    G, splits = _groups(m_splits, i)
+    ws, ws_bytes = _workspace(workspace, i)
+    _run("te_moe_sort", (
+        _addr(experts, "experts", shape, "int32", i), slots, G, splits, _addr(row_of, "row_of", shape, "int32", i),
+        _addr(slot_of, "slot_of", (slots,), "int32", i), ws, ws_bytes), i, stream)
+
+
+def _rows_args(row_of, tokens, index):
+    """(topk, address) of row_of [tokens, topk]."""
+    _require(row_of is not None and row_of.dim() == 2, "row_of: expected a 2-D int32 tensor")
+    topk = row_of.shape[1]
+    return topk, _addr(row_of, "row_of", (tokens, topk), "int32", index)
+
+
+def _rows_out(y, q, q_scale, dtype, cols, index, name):
+    """(rows in all, addresses of y, q and q_scale) of the outputs with a row each slot."""
+    _require(y is not None or q is not None, f"{name} or q is required")
+    first = y if y is not None else q
+    _require(first.dim() == 2, f"{name}: expected a 2-D tensor")
+    rows = first.shape[0]
+    if q is not None:
+        _require(cols % 32 == 0, "q: the MXFP8 output needs cols % 32 == 0")
+    return (rows, _opt(y, name, (rows, cols), dtype, index), _opt(q, "q", (rows, cols), _CODES, index),
+            _opt(q_scale, "q_scale", (rows, cols // 32), _CODES, index))
+
+
+def _float_2d(t, name):
+    index = _index_of(t, name)
+    _require(t.dtype in _NORM_DTYPES, f"{name}: expected {_FLOATS}, got {t.dtype}")
+    return index, t.dtype, t.shape
+
+
+def te_moe_dispatch(x, row_of, y=None, q=None, q_scale=None, q_fmt="e4m3", stream=None) -> None:
+    i, xd, (tokens, cols) = _float_2d(x, "x")
+    topk, row_at = _rows_args(row_of, tokens, i)
+    rows, py, pq, pqs = _rows_out(y, q, q_scale, xd, cols, i, "y")
+    _run("te_moe_dispatch", (_addr(x, "x", (tokens, cols), xd, i), _NORM_DTYPES[xd], tokens, cols, row_at, topk, rows,
+                             py, pq, pqs, _fmt(q_fmt)), i, stream)
+
+
+def te_moe_combine(rows, row_of, y, weights=None, stream=None) -> None:
+    """weights None: all 1, the gradient of te_moe_dispatch."""
+    i, xd, (total, cols) = _float_2d(rows, "rows")
+    _require(y is not None and y.dim() == 2, "y: expected a 2-D tensor")
+    tokens = y.shape[0]
+    topk, row_at = _rows_args(row_of, tokens, i)
+    _run("te_moe_combine", (_addr(rows, "rows", (total, cols), xd, i), _NORM_DTYPES[xd], total, cols, row_at,
+                            _opt(weights, "weights", (tokens, topk), "float32", i), tokens, topk,
+                            _addr(y, "y", (tokens, cols), xd, i)), i, stream)
+
+
+def te_moe_combine_backward(dy, rows, row_of, weights, dweights, drows=None, q=None, q_scale=None, q_fmt="e5m2",
+                            stream=None) -> None:
+    i, xd, (tokens, cols) = _float_2d(dy, "dy")
+    topk, row_at = _rows_args(row_of, tokens, i)
+    total, pd, pq, pqs = _rows_out(drows, q, q_scale, xd, cols, i, "drows")
+    _run("te_moe_combine_backward", (
+        _addr(dy, "dy", (tokens, cols), xd, i), _addr(rows, "rows", (total, cols), xd, i), _NORM_DTYPES[xd], tokens,
+        cols, row_at, _addr(weights, "weights", (tokens, topk), "float32", i), topk, total, pd, pq, pqs, _fmt(q_fmt),
+        _addr(dweights, "dweights", (tokens, topk), "float32", i)), i, stream)
+
+
+# ------------------------------------------------------ GEMMs with 4-bit weights
+
+_W4_SCALES = {torch.bfloat16: TE_BF16, torch.float16: TE_FP16, torch.float32: TE_FP32, torch.uint8: TE_E8M0}
+_W4_SCALES |= {getattr(torch, n): TE_E8M0 for n in ("float8_e8m0fnu",) if hasattr(torch, n)}
+_KINDS["a scale type"] = frozenset(_W4_SCALES)
+
+
+def _w4_args(x, w, w_fmt, w_scale, zero, rows, d, n):
+    """(device index, the arguments up to the group size, M, K, d's address and dtype) of rows x K weights."""
+    i = _index_of(x, "x")
+    _require(x.dtype in (torch.bfloat16, torch.float16), f"x: expected bfloat16 or float16, got {x.dtype}")
+    M, K = x.shape
+    _require(w_scale is not None and w_scale.dim() == 2, "w_scale must be 2-D")
+    scales = w_scale.shape[1]
+    _require(scales > 0 and K % scales == 0 if K else scales == 0,
+             f"w_scale: {scales} columns do not divide K = {K} into groups")
+    dt = _NORM_DTYPES[x.dtype]
+    scale_dt = _W4_SCALES.get(w_scale.dtype)
+    _require(scale_dt is not None and (scale_dt != TE_BF16 and scale_dt != TE_FP16 or scale_dt == dt),
+             f"w_scale: expected x's dtype, float32 or E8M0 codes (uint8), got {w_scale.dtype}")
+    _require(d is not None and (d.dtype == x.dtype or d.dtype == torch.float32), "d: expected x's dtype or float32")
+    _require(K % 2 == 0, "w: K must be even (two codes a byte)")
+    args = (_addr(x, "x", (M, K), x.dtype, i), dt, _addr(w, "w", (rows, K // 2), _CODES, i),
+            W4_FORMATS[w_fmt] if isinstance(w_fmt, str) else int(w_fmt),
+            _addr(w_scale, "w_scale", (rows, scales), "a scale type", i), scale_dt,
+            _opt(zero, "zero", (rows, scales), _CODES, i), K // scales if scales else 32)
+    return i, args, M, K, _addr(d, "d", (M, n), d.dtype, i), _NORM_DTYPES[d.dtype]
+
+
+def _rows_of(t, name, per=1):
+    _require(t is not None and t.dim() == 2, f"{name} must be 2-D")
+    _require(t.shape[0] % per == 0, f"{name}: expected an even number of rows (gate rows, then up rows)")
+    return t.shape[0] // per
+
+
+def te_w4_gemm(x, w, w_fmt, w_scale, d, zero=None, bias=None, stream=None) -> None:
+    """w uint8 [N, K/2] ("int4" or "e2m1" codes, even k in the low half), w_scale [N, groups of K], zero uint8 likewise."""
+    N = _rows_of(w, "w")
+    i, args, M, K, pd, dd = _w4_args(x, w, w_fmt, w_scale, zero, N, d, N)
+    _run("te_w4_gemm", (*args, M, N, K, pd, dd, _opt(bias, "bias", (N,), x.dtype, i)), i, stream)
+
+
+def te_w4_gated_gemm(x, w, w_fmt, w_scale, d, activation="silu", zero=None, bias=None, stream=None) -> None:
+    N = _rows_of(w, "w", 2)
+    i, args, M, K, pd, dd = _w4_args(x, w, w_fmt, w_scale, zero, 2 * N, d, N)
+    _run("te_w4_gated_gemm", (*args, M, N, K, _activation(activation), pd, dd,
+                              _opt(bias, "bias", (2 * N,), x.dtype, i)), i, stream)
+
+
+def te_w4_grouped_gemm(m_splits, x, w, w_fmt, w_scale, n: int, d, zero=None, bias=None, stream=None) -> None:
+    i, n = _index_of(x, "x"), int(n)
+    G, splits = _groups(m_splits, i)
+    _, args, M, K, pd, dd = _w4_args(x, w, w_fmt, w_scale, zero, G * n, d, n)
+    _run("te_w4_grouped_gemm", (G, splits, M, *args, n, K, pd, dd, _opt(bias, "bias", (G, n), x.dtype, i)), i, stream)
+
+
+def te_w4_grouped_gated_gemm(m_splits, x, w, w_fmt, w_scale, n: int, d, activation="silu", zero=None, bias=None,
+                             stream=None) -> None:
+    i, n = _index_of(x, "x"), int(n)
+    G, splits = _groups(m_splits, i)
+    _, args, M, K, pd, dd = _w4_args(x, w, w_fmt, w_scale, zero, G * 2 * n, d, n)
+    _run("te_w4_grouped_gated_gemm", (G, splits, M, *args, n, K, _activation(activation), pd, dd,
+                                      _opt(bias, "bias", (G, 2 * n), x.dtype, i)), i, stream)
+
+
 # ------------------------------------------------------- allocating helpers
 
 def mxfp8_quantize(x, fmt="e4m3", direction="row", stream=None):
@@ -822,4 +1013,87 @@ def mxfp8_dgated_gemm(a, a_scale, a_fmt, b, b_scale, b_fmt, aux, activation="sil
         size = te_mxfp8_dgated_gemm_workspace_size(M, N, K)
         ws = torch.empty(size, dtype=torch.uint8, device=a.device) if size else None
         te_mxfp8_dgated_gemm(a, a_scale, a_fmt, b, b_scale, b_fmt, aux, d, activation, ws, stream)
+    return d
+
+
+def moe_route(score, logits, topk, bias=None, normalize=True, scale=1.0, stream=None):
+    """The router ("softmax" or "sigmoid" scores) -> (experts int32 [tokens, topk], weights float32 [tokens, topk])."""
+    with _allocating_on(stream, logits.device):
+        experts = torch.empty((logits.shape[0], topk), dtype=torch.int32, device=logits.device)
+        weights = torch.empty((logits.shape[0], topk), dtype=torch.float32, device=logits.device)
+        te_moe_route(score, logits, experts, weights, bias, normalize, scale, stream)
+    return experts, weights
+
+
+def moe_route_backward(score, logits, experts, dweights, normalize=True, scale=1.0, stream=None):
+    """-> dlogits, the gradient of the logits from moe_route's weights' one."""
+    with _allocating_on(stream, logits.device):
+        dlogits = torch.empty_like(logits)
+        te_moe_route_backward(score, logits, experts, dweights, dlogits, normalize, scale, stream)
+    return dlogits
+
+
+def moe_sort(experts, num_experts: int, stream=None):
+    """experts int32 [tokens, topk] -> (m_splits [num_experts], row_of [tokens, topk], slot_of [tokens * topk])."""
+    dev = experts.device
+    with _allocating_on(stream, dev):
+        m_splits = torch.empty(num_experts, dtype=torch.int32, device=dev)
+        row_of = torch.empty_like(experts)
+        slot_of = torch.empty(experts.numel(), dtype=torch.int32, device=dev)
+        size = te_moe_sort_workspace_size(experts.numel(), num_experts)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+        te_moe_sort(experts, m_splits, row_of, slot_of, ws, stream)
+    return m_splits, row_of, slot_of
+
+
+def moe_dispatch(x, row_of, mx_fmt=None, want_y=True, stream=None):
+    """Each token's row at its slots' rows -> (y, q, q_scale) with tokens * topk rows: y in x's dtype (None if not
+    wanted), the MXFP8 operand with mx_fmt.  Rows behind the last are unset."""
+    rows, cols, dev = row_of.numel(), x.shape[1], x.device
+    with _allocating_on(stream, dev):
+        y = torch.empty((rows, cols), dtype=x.dtype, device=dev) if want_y else None
+        q = torch.empty((rows, cols), dtype=torch.uint8, device=dev) if mx_fmt else None
+        qs = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev) if mx_fmt else None
+        te_moe_dispatch(x, row_of, y, q, qs, mx_fmt or "e4m3", stream)
+    return y, q, qs
+
+
+def moe_combine(rows, row_of, weights=None, stream=None):
+    """-> y [tokens, cols], each token's rows added up with its weights (None: all 1, the gradient of moe_dispatch)."""
+    with _allocating_on(stream, rows.device):
+        y = torch.empty((row_of.shape[0], rows.shape[1]), dtype=rows.dtype, device=rows.device)
+        te_moe_combine(rows, row_of, y, weights, stream)
+    return y
+
+
+def moe_combine_backward(dy, rows, row_of, weights, mx_fmt=None, want_drows=True, stream=None):
+    """-> (drows, dweights, q, q_scale): drows in dy's dtype (None if not wanted), its MXFP8 operand with mx_fmt.  Rows
+    behind the last are unset."""
+    total, cols, dev = rows.shape[0], rows.shape[1], rows.device
+    with _allocating_on(stream, dev):
+        drows = torch.empty_like(rows) if want_drows else None
+        q = torch.empty((total, cols), dtype=torch.uint8, device=dev) if mx_fmt else None
+        qs = torch.empty((total, cols // 32), dtype=torch.uint8, device=dev) if mx_fmt else None
+        dweights = torch.empty_like(weights)
+        te_moe_combine_backward(dy, rows, row_of, weights, dweights, drows, q, qs, mx_fmt or "e5m2", stream)
+    return drows, dweights, q, qs
+
+
+def w4_gemm(x, w, w_fmt, w_scale, zero=None, bias=None, activation=None, m_splits=None, out_dtype=None, stream=None):
+    """x W^T of 4-bit weights (te_w4_gemm); with an activation the gated form (w = [gate rows; up rows]), with m_splits
+    the grouped one (the experts' weights stacked) -> D in x's dtype or out_dtype."""
+    M, dev = x.shape[0], x.device
+    per = (m_splits.numel() if m_splits is not None else 1) * (2 if activation else 1)
+    n = w.shape[0] // per
+    with _allocating_on(stream, dev):
+        d = torch.empty((M, n), dtype=out_dtype or x.dtype, device=dev)
+        more = {"zero": zero, "bias": bias, "stream": stream}
+        if m_splits is not None and activation:
+            te_w4_grouped_gated_gemm(m_splits, x, w, w_fmt, w_scale, n, d, activation, **more)
+        elif m_splits is not None:
+            te_w4_grouped_gemm(m_splits, x, w, w_fmt, w_scale, n, d, **more)
+        elif activation:
+            te_w4_gated_gemm(x, w, w_fmt, w_scale, d, activation, **more)
+        else:
+            te_w4_gemm(x, w, w_fmt, w_scale, d, **more)
     return d

@@ -1,0 +1,466 @@
+// The router of a mixture-of-experts block and the sort of its slots by expert, for gfx950.
+//
+// With l the logits of a token and s_e = softmax(l)_e over its experts that are not masked (l_e > -inf), or
+// sigmoid(l_e), the chosen experts e_0, e_1, .. are the topk largest of s_e + bias_e (of l_e without a bias: the scores
+// rise with the logits) in falling order, equal ones in rising order of e, and
+//   w_k = scale s_{e_k} / S,   S = sum over the chosen of s, or 1 (normalize = 0).
+// Backward, with g_k = scale dw_k:
+//   ds_k = (g_k - sum_j g_j w_j / scale) / S   (normalize = 0: ds_k = g_k)
+//   sigmoid:  dl_e = ds_e s_e (1 - s_e)
+//   softmax:  dl_e = s_e (ds_e - sum_j ds_j s_j)   (normalize: the sum is 0, only the chosen have a gradient)
+#include <type_traits>
+
+#include "row_chunks.h"
+
+namespace temx {
+namespace {
+
+constexpr int kRouteThreads = 256;
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxTopk = 64;
+constexpr int kNoExpert = 0x7FFFFFFF;
+
+struct RouteParams {
+  const void* logits;
+  const float* bias;
+  int32_t* experts;        // written by the forward, read by the backward
+  float* weights;          // forward
+  const float* dweights;   // backward
+  void* dlogits;           // backward
+  int64_t tokens;
+  int num_experts, topk;
+  float scale;
+  bool sigmoid, normalize;
+};
+
+// The lane's value against those of the other lanes of its LANES (16 or 64): op over all, in every lane.
+template <int LANES, class V, class Op>
+__device__ __forceinline__ V lanes_all(V v, Op op) {
+  auto ror = [](V x, auto n) {
+    constexpr int kWords = sizeof(V) / 4;
+    struct Words { int w[kWords]; } u = __builtin_bit_cast(Words, x);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) u.w[i] = __builtin_amdgcn_mov_dpp(u.w[i], 0x120 + decltype(n)::value, 0xF, 0xF, false);
+    return __builtin_bit_cast(V, u);
+  };
+  v = op(v, ror(v, std::integral_constant<int, 8>{}));  // row_ror within 16 lanes
+  v = op(v, ror(v, std::integral_constant<int, 4>{}));
+  v = op(v, ror(v, std::integral_constant<int, 2>{}));
+  v = op(v, ror(v, std::integral_constant<int, 1>{}));
+  if constexpr (LANES == 64) {
+    v = op(v, __shfl_xor(v, 16));
+    v = op(v, __shfl_xor(v, 32));
+  }
+  return v;
+}
+
+template <class T>
+__device__ __forceinline__ float load_logit(const void* p, int64_t i) { return to_float(static_cast<const T*>(p)[i]); }
+template <>
+__device__ __forceinline__ float load_logit<float>(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
+
+constexpr float kInf = __builtin_huge_valf();
+
+// 1 / (1 + e^-x) and its derivative, without cancellation on either side.
+__device__ __forceinline__ float sigmoid_of(float x) { return 1.0f / (1.0f + expf(-x)); }
+__device__ __forceinline__ float sigmoid_slope(float x) {
+  const float e = expf(-fabsf(x));
+  return e / ((1.0f + e) * (1.0f + e));
+}
+
+// LANES lanes a token, V experts a lane (expert v LANES + lane).  The keys are the logits themselves, or with a bias
+// s + bias in 64 bits: two experts' keys may lie closer than 32 bits tell apart.  A slot a round: the largest key, then
+// the lowest expert that has it; the lane of that number keeps it.
+template <class T, int LANES, int V, bool BIAS>
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteParams p) {
+  typedef std::conditional_t<BIAS, double, float> Key;
+  constexpr Key kNone = -(Key)kInf;
+  const int lane = threadIdx.x % LANES;
+  const int64_t token = (int64_t)blockIdx.x * (kRouteThreads / LANES) + threadIdx.x / LANES;
+  const bool ok = token < p.tokens;  // every lane takes part in the exchanges
+  const int64_t at = (ok ? token : 0) * p.num_experts;
+  const auto most = [](auto a, auto b) { return a > b ? a : b; };  // keys are never NaN here
+  const auto sum = [](auto a, auto b) { return a + b; };
+
+  Key key[V];
+  float top = 0.f, total = 1.f;  // softmax: the largest logit, sum of e^(l - top)
+  {
+    float l[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = v * LANES + lane < p.num_experts ? load_logit<T>(p.logits, at + v * LANES + lane) : -kInf;
+    if (!p.sigmoid && (BIAS || !p.normalize)) {
+      float m = -kInf;
+#pragma unroll
+      for (int v = 0; v < V; ++v) m = fmaxf(m, l[v]);
+      m = lanes_all<LANES>(m, most);
+      top = m > -kInf ? m : 0.f;
+      float s = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) s += expf(l[v] - top);
+      total = lanes_all<LANES>(s, sum);
+    }
+    if constexpr (BIAS) {
+      double sum64 = 1.0;
+      if (!p.sigmoid) {
+        sum64 = 0.0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) sum64 += exp((double)l[v] - (double)top);
+        sum64 = lanes_all<LANES>(sum64, sum);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int e = v * LANES + lane;
+        const double s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l[v])) : exp((double)l[v] - (double)top) / sum64;
+        const double k = l[v] > -kInf && e < p.num_experts ? s + (double)p.bias[e] : kNone;
+        key[v] = k > kNone ? k : kNone;  // NaN too
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = l[v] > kNone ? l[v] : kNone;
+    }
+  }
+
+  int mine = -1;
+  for (int k = 0; k < p.topk; ++k) {
+    Key best = key[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) best = most(best, key[v]);
+    best = lanes_all<LANES>(best, most);
+    int e = kNoExpert;
+#pragma unroll
+    for (int v = V - 1; v >= 0; --v) e = key[v] == best ? v * LANES + lane : e;
+    e = lanes_all<LANES>(e, [](int a, int b) { return a < b ? a : b; });
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = v * LANES + lane == e ? kNone : key[v];
+    if (lane == k) mine = best > kNone ? e : -1;
+  }
+
+  const float l = mine >= 0 ? load_logit<T>(p.logits, at + mine) : -kInf;
+  float w;
+  if (p.sigmoid) {
+    w = mine >= 0 ? sigmoid_of(l) : 0.f;
+  } else {
+    if (p.normalize) {
+      const float m = lanes_all<LANES>(l, [](float a, float b) { return fmaxf(a, b); });
+      top = m > -kInf ? m : 0.f;
+    }
+    w = mine >= 0 ? expf(l - top) : 0.f;
+  }
+  if (p.normalize) total = lanes_all<LANES>(w, sum);
+  if (p.normalize || !p.sigmoid) w = w == 0.f && total == 0.f ? 0.f : w / total;
+  if (ok && lane < p.topk) {
+    p.experts[token * p.topk + lane] = mine;
+    p.weights[token * p.topk + lane] = p.scale * w;
+  }
+}
+
+// LANES lanes a token as in the forward.  The slots' gradients meet the experts' lanes in LDS (two slots that name one
+// expert are added).
+template <class T, int LANES, int V>
+__global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteParams p) {
+  __shared__ float slots[kRouteThreads / LANES][V * LANES];
+  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  const int64_t token = (int64_t)blockIdx.x * (kRouteThreads / LANES) + group;
+  const bool ok = token < p.tokens;
+  const int64_t at = (ok ? token : 0) * p.num_experts;
+  const auto sum = [](float a, float b) { return a + b; };
+  const auto most = [](float a, float b) { return fmaxf(a, b); };
+#pragma unroll
+  for (int v = 0; v < V; ++v) slots[group][v * LANES + lane] = 0.f;
+
+  int e = -1;
+  float g = 0.f, l = -kInf;
+  if (ok && lane < p.topk) {
+    e = p.experts[token * p.topk + lane];
+    if ((unsigned)e >= (unsigned)p.num_experts) e = -1;
+    if (e >= 0) {
+      g = p.scale * p.dweights[token * p.topk + lane];
+      l = load_logit<T>(p.logits, at + e);
+    }
+  }
+  const bool all = !p.sigmoid && !p.normalize;  // every expert's logit has a gradient
+  float x[V], top = 0.f, total = 1.f;
+  if (all) {
+    float m = -kInf;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      x[v] = v * LANES + lane < p.num_experts ? load_logit<T>(p.logits, at + v * LANES + lane) : -kInf;
+      m = fmaxf(m, x[v]);
+    }
+    m = lanes_all<LANES>(m, most);
+    top = m > -kInf ? m : 0.f;
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      x[v] = expf(x[v] - top);
+      s += x[v];
+    }
+    total = lanes_all<LANES>(s, sum);
+    total = total == 0.f ? 1.f : total;
+  } else if (!p.sigmoid) {
+    const float m = lanes_all<LANES>(l, most);
+    top = m > -kInf ? m : 0.f;
+  }
+  // the slot's score (of shares among the chosen: up to the factor that cancels)
+  const float s = e < 0 ? 0.f : p.sigmoid ? sigmoid_of(l) : expf(l - top) / total;
+  float c = 0.f;  // what every expert subtracts
+  if (p.normalize) {
+    float S = lanes_all<LANES>(s, sum);
+    S = S == 0.f ? 1.f : S;
+    const float gw = lanes_all<LANES>(g * s, sum) / S;
+    g = e < 0 ? 0.f : (g - gw) / S;
+    if (!p.sigmoid) g *= s;
+  } else if (!p.sigmoid) {
+    c = lanes_all<LANES>(g * s, sum);
+  }
+  if (p.sigmoid && e >= 0) g *= sigmoid_slope(l);
+  __syncthreads();
+  if (e >= 0) atomicAdd(&slots[group][e], g);
+  __syncthreads();
+  if (!ok) return;
+  T* out = static_cast<T*>(p.dlogits) + at;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int j = v * LANES + lane;
+    if (j >= p.num_experts) continue;
+    const float d = slots[group][j];
+    out[j] = from_float<T>(all ? x[v] / total * (d - c) : d);
+  }
+}
+
+// ---- the sort ---------------------------------------------------------------
+
+// A stable counting sort: the slots in runs, a workgroup each; a run's slots in parts, a wave each.
+constexpr int kSortWaves = 8;
+constexpr int kSortThreads = 64 * kSortWaves;
+constexpr int kSortRun = 2048;    // slots of a workgroup, more where kSortBlocks of them do not suffice
+constexpr int kSortBlocks = 256;
+
+int64_t sort_run(int64_t slots) {
+  const int64_t run = (slots + kSortBlocks - 1) / kSortBlocks;
+  return run <= kSortRun ? kSortRun : (run + kSortRun - 1) / kSortRun * kSortRun;
+}
+int64_t sort_blocks(int64_t slots) { return (slots + sort_run(slots) - 1) / sort_run(slots); }
+
+struct SortParams {
+  const int32_t* experts;
+  int32_t* m_splits;
+  int32_t* row_of;
+  int32_t* slot_of;
+  int32_t* counts;  // [blocks][num_experts], of the runs (more than one)
+  int64_t slots, run;
+  int num_experts, blocks;
+};
+
+// Each run's slots per expert.
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortParams p) {
+  __shared__ int count[kMaxExperts];
+  for (int e = threadIdx.x; e < p.num_experts; e += kSortThreads) count[e] = 0;
+  __syncthreads();
+  const int64_t begin = blockIdx.x * p.run, end = min(begin + p.run, p.slots);
+  for (int64_t i = begin + threadIdx.x; i < end; i += kSortThreads) {
+    const int e = p.experts[i];
+    if ((unsigned)e < (unsigned)p.num_experts) atomicAdd(&count[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.num_experts; e += kSortThreads) p.counts[(int64_t)blockIdx.x * p.num_experts + e] = count[e];
+}
+
+// Lanes of the wave whose value equals the lane's own, in the low `bits` bits.
+__device__ __forceinline__ uint64_t same_lanes(int v, int bits) {
+  uint64_t same = ~0ull;
+  for (int b = 0; b < bits; ++b) {
+    const uint64_t set = __ballot((v >> b) & 1);
+    same &= (v >> b) & 1 ? set : ~set;
+  }
+  return same;
+}
+
+// The rows of a run's slots: the rows of smaller experts, of the expert's slots in earlier runs, in the run's earlier
+// parts and in the part before the slot.  Every workgroup adds up the counts it needs by itself.
+__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortParams p) {
+  __shared__ int part[kSortWaves][kMaxExperts];  // slots of a wave's part; then the next row of each expert in it
+  __shared__ int wave_sum[kSortWaves];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t begin = blockIdx.x * p.run, share = p.run / kSortWaves;
+  const int64_t part_begin = begin + wave * share, part_end = min(part_begin + share, p.slots);
+  for (int e = threadIdx.x; e < kSortWaves * kMaxExperts; e += kSortThreads) part[0][e] = 0;
+  __syncthreads();
+  for (int64_t i = part_begin + lane; i < part_end; i += 64) {
+    const int e = p.experts[i];
+    if ((unsigned)e < (unsigned)p.num_experts) atomicAdd(&part[wave][e], 1);
+  }
+  __syncthreads();
+  // two experts a thread: 2 t, 2 t + 1
+  int total[2] = {0, 0}, before[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int e = 2 * threadIdx.x + j;
+    if (e >= p.num_experts) continue;
+    if (p.blocks == 1) {
+      for (int w = 0; w < kSortWaves; ++w) total[j] += part[w][e];
+    } else {
+      for (int b = 0; b < p.blocks; ++b) {
+        const int c = p.counts[(int64_t)b * p.num_experts + e];
+        total[j] += c;
+        before[j] += b < (int)blockIdx.x ? c : 0;
+      }
+    }
+  }
+  // rows of the smaller experts: a scan over the threads
+  int scan = total[0] + total[1];
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int up = __shfl_up(scan, d);
+    scan += lane >= d ? up : 0;
+  }
+  if (lane == 63) wave_sum[wave] = scan;
+  __syncthreads();
+  int rows = 0, first = scan - total[0] - total[1];
+  for (int w = 0; w < kSortWaves; ++w) {
+    first += w < wave ? wave_sum[w] : 0;
+    rows += wave_sum[w];
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int e = 2 * threadIdx.x + j;
+    if (e >= p.num_experts) continue;
+    if (blockIdx.x == 0) p.m_splits[e] = total[j];
+    int row = first + (j == 1 ? total[0] : 0) + before[j];
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int n = part[w][e];
+      part[w][e] = row;
+      row += n;
+    }
+  }
+  __syncthreads();
+  int bits = 1;
+  while ((1 << bits) <= p.num_experts) ++bits;  // the experts and one more value
+  for (int64_t i0 = part_begin; i0 < part_end; i0 += 64) {
+    const int64_t i = i0 + lane;
+    int e = i < part_end ? p.experts[i] : -1;
+    const bool valid = (unsigned)e < (unsigned)p.num_experts;
+    e = valid ? e : p.num_experts;
+    const uint64_t same = same_lanes(e, bits);
+    const int rank = __popcll(same & ((1ull << lane) - 1));
+    int row = -1;
+    if (valid) {
+      row = part[wave][e] + rank;
+      p.slot_of[row] = (int)i;
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (valid && rank == 0) part[wave][e] = row + __popcll(same);
+    if (i < part_end) p.row_of[i] = row;
+    __builtin_amdgcn_wave_barrier();
+  }
+  for (int64_t r = begin + threadIdx.x; r < min(begin + p.run, p.slots); r += kSortThreads)
+    if (r >= rows) p.slot_of[r] = -1;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+template <class T, int LANES, int V>
+te_status launch_route(const RouteParams& p, bool backward, hipStream_t stream) {
+  constexpr int kPer = kRouteThreads / LANES;
+  const dim3 grid((unsigned)((p.tokens + kPer - 1) / kPer)), block(kRouteThreads);
+  if (backward) hipLaunchKernelGGL((route_backward_kernel<T, LANES, V>), grid, block, 0, stream, p);
+  else if (p.bias != nullptr) hipLaunchKernelGGL((route_kernel<T, LANES, V, true>), grid, block, 0, stream, p);
+  else hipLaunchKernelGGL((route_kernel<T, LANES, V, false>), grid, block, 0, stream, p);
+  return launch_status();
+}
+
+template <class T>
+te_status run_route(const RouteParams& p, bool backward, hipStream_t stream) {
+  if (p.topk <= 16 && p.num_experts <= 256) {
+    if (p.num_experts <= 32) return launch_route<T, 16, 2>(p, backward, stream);
+    if (p.num_experts <= 64) return launch_route<T, 16, 4>(p, backward, stream);
+    if (p.num_experts <= 128) return launch_route<T, 16, 8>(p, backward, stream);
+    return launch_route<T, 16, 16>(p, backward, stream);
+  }
+  if (p.num_experts <= 256) return launch_route<T, 64, 4>(p, backward, stream);
+  if (p.num_experts <= 512) return launch_route<T, 64, 8>(p, backward, stream);
+  return launch_route<T, 64, 16>(p, backward, stream);
+}
+
+te_status run_route(const RouteParams& p, te_dtype dtype, bool backward, hipStream_t stream) {
+  if (dtype == TE_BF16) return run_route<bf16_t>(p, backward, stream);
+  if (dtype == TE_FP16) return run_route<f16_t>(p, backward, stream);
+  return run_route<float>(p, backward, stream);
+}
+
+constexpr int64_t kMostSlots = ((int64_t)1 << 31) - 65536;
+
+te_status check_route(te_score score, te_dtype dtype, int64_t tokens, int num_experts, int topk, int normalize, float scale) {
+  TE_REQUIRE(score == TE_SCORE_SOFTMAX || score == TE_SCORE_SIGMOID, TE_ERR_VALUE);
+  TE_REQUIRE((normalize == 0 || normalize == 1) && fabsf(scale) <= 3.0e38f, TE_ERR_VALUE);
+  TE_REQUIRE(dtype == TE_BF16 || dtype == TE_FP16 || dtype == TE_FP32, TE_ERR_DTYPE);
+  TE_REQUIRE(num_experts >= 1 && num_experts <= kMaxExperts, TE_ERR_SHAPE);
+  TE_REQUIRE(topk >= 1 && topk <= num_experts && topk <= kMaxTopk, TE_ERR_SHAPE);
+  TE_REQUIRE(tokens >= 0 && tokens <= kMostSlots / topk, TE_ERR_SHAPE);
+  return TE_OK;
+}
+
+}  // namespace
+}  // namespace temx
+
+using namespace temx;
+
+extern "C" te_status te_moe_route(te_score score, const void* logits, te_dtype dtype, int64_t tokens,
+                                  int32_t num_experts, int32_t topk, const float* bias, int normalize, float scale,
+                                  int32_t* experts, float* weights, hipStream_t stream) {
+  const te_status st = check_route(score, dtype, tokens, num_experts, topk, normalize, scale);
+  if (st != TE_OK) return st;
+  if (tokens == 0) return TE_OK;
+  TE_REQUIRE(logits && experts && weights, TE_ERR_NULL);
+  TE_REQUIRE(aligned16(logits) && aligned4(bias) && aligned4(experts) && aligned4(weights), TE_ERR_ALIGN);
+  TE_REQUIRE(device_is_gfx950(), TE_ERR_ARCH);
+  const RouteParams p{logits, bias, experts, weights, nullptr, nullptr, tokens, num_experts, topk, scale,
+                      score == TE_SCORE_SIGMOID, normalize != 0};
+  return run_route(p, dtype, false, stream);
+}
+
+extern "C" te_status te_moe_route_backward(te_score score, const void* logits, te_dtype dtype, int64_t tokens,
+                                           int32_t num_experts, int32_t topk, int normalize, float scale,
+                                           const int32_t* experts, const float* dweights, void* dlogits,
+                                           hipStream_t stream) {
+  const te_status st = check_route(score, dtype, tokens, num_experts, topk, normalize, scale);
+  if (st != TE_OK) return st;
+  if (tokens == 0) return TE_OK;
+  TE_REQUIRE(logits && experts && dweights && dlogits, TE_ERR_NULL);
+  TE_REQUIRE(aligned16(logits) && aligned16(dlogits) && aligned4(experts) && aligned4(dweights), TE_ERR_ALIGN);
+  TE_REQUIRE(device_is_gfx950(), TE_ERR_ARCH);
+  const RouteParams p{logits, nullptr, const_cast<int32_t*>(experts), nullptr, dweights, dlogits, tokens, num_experts,
+                      topk, scale, score == TE_SCORE_SIGMOID, normalize != 0};
+  return run_route(p, dtype, true, stream);
+}
+
+extern "C" size_t te_moe_sort_workspace_size(int64_t slots, int32_t num_experts) {
+  if (slots <= 0 || slots > kMostSlots || num_experts < 1 || num_experts > kMaxExperts) return 0;
+  const int64_t blocks = sort_blocks(slots);
+  return blocks == 1 ? 0 : (size_t)(blocks * num_experts) * sizeof(int32_t);
+}
+
+extern "C" te_status te_moe_sort(const int32_t* experts, int64_t slots, int32_t num_experts, int32_t* m_splits,
+                                 int32_t* row_of, int32_t* slot_of, void* workspace, size_t workspace_bytes,
+                                 hipStream_t stream) {
+  TE_REQUIRE(num_experts >= 1 && num_experts <= kMaxExperts, TE_ERR_SHAPE);
+  TE_REQUIRE(slots >= 0 && slots <= kMostSlots, TE_ERR_SHAPE);
+  TE_REQUIRE(m_splits != nullptr && (slots == 0 || (experts && row_of && slot_of)), TE_ERR_NULL);
+  TE_REQUIRE(aligned4(experts) && aligned4(m_splits) && aligned4(row_of) && aligned4(slot_of), TE_ERR_ALIGN);
+  const int blocks = slots == 0 ? 1 : (int)sort_blocks(slots);
+  if (blocks > 1) {
+    TE_REQUIRE(workspace != nullptr, TE_ERR_NULL);
+    TE_REQUIRE(aligned4(workspace), TE_ERR_ALIGN);
+    TE_REQUIRE(workspace_bytes >= te_moe_sort_workspace_size(slots, num_experts), TE_ERR_WORKSPACE);
+  }
+  TE_REQUIRE(device_is_gfx950(), TE_ERR_ARCH);
+  const SortParams p{experts, m_splits, row_of, slot_of, static_cast<int32_t*>(workspace), slots, sort_run(slots),
+                     num_experts, blocks};
+  if (blocks > 1) {
+    hipLaunchKernelGGL(sort_count_kernel, dim3(blocks), dim3(kSortThreads), 0, stream, p);
+    const te_status st = launch_status();
+    if (st != TE_OK) return st;
+  }
+  hipLaunchKernelGGL(sort_place_kernel, dim3(blocks), dim3(kSortThreads), 0, stream, p);
+  return launch_status();
+}

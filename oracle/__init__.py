@@ -45,6 +45,8 @@ from .blockwise import quantize_1d, quantize_2d, block_gemm, pow2_at_least, e8m0
 from .gemm import mx_gemm, gelu_tanh, dgelu_tanh, epilogue, grouped_mx_gemm, within_tolerance, tolerance_bound
 from .norm import norm_forward, norm_backward
 from .gated import activation, activation_grad, gated, gated_grad
+from .moe import scores, route, shares, route_backward, sort_slots, combine, combine_backward
+from .w4 import unpack_codes, e2m1_decode, w4_values, w4_gemm
 
 __all__ = [
     "E4M3", "E5M2", "FP8Format", "decode", "encode", "e8m0_decode", "format_by_name",
@@ -52,4 +54,6 @@ __all__ = [
     "amax", "current_scale", "cast_current_scaling",
     "mx_gemm", "gelu_tanh", "epilogue", "grouped_mx_gemm", "within_tolerance", "tolerance_bound",
     "norm_forward", "norm_backward", "activation", "activation_grad", "gated", "gated_grad",
+    "scores", "route", "shares", "route_backward", "sort_slots", "combine", "combine_backward",
+    "unpack_codes", "e2m1_decode", "w4_values", "w4_gemm",
 ]
