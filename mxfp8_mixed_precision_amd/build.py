@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libtemx.so")
 SOURCES = ["quantize.hip", "amax_cast.hip", "gemm.hip", "block_gemm.hip", "block_gemm_e8m0.hip", "block_gemm_fp32.hip", "block_scale.hip",
            "block_quantize.hip", "norm.hip", "gated_gemm.hip",
-           "gated_gemm4.hip", "gated_rows.hip", "moe_route.hip", "moe_rows.hip", "w4_gemm.hip", "status.hip"]
+           "gated_gemm4.hip", "gated_rows.hip", "moe_route.hip", "moe_rows.hip", "w4_gemm.hip", "w4_bf16_int4.hip",
+           "w4_bf16_e2m1.hip", "w4_fp16_int4.hip", "w4_fp16_e2m1.hip", "status.hip"]
 ARCH = "gfx950"
 
 
