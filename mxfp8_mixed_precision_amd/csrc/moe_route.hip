@@ -33,23 +33,40 @@ struct RouteParams {
   bool sigmoid, normalize;
 };
 
-// The lane's value against those of the other lanes of its LANES (16 or 64): op over all, in every lane.
+// op over the values of the lane's LANES (16, 32 or 64) lanes, in every lane.
 template <int LANES, class V, class Op>
 __device__ __forceinline__ V lanes_all(V v, Op op) {
-  auto ror = [](V x, auto n) {
-    constexpr int kWords = sizeof(V) / 4;
-    struct Words { int w[kWords]; } u = __builtin_bit_cast(Words, x);
+  constexpr int kWords = sizeof(V) / 4;
+  struct Words {
+    int w[kWords];
+  };
+  const auto ror = [](V x, auto n) {  // row_ror within 16 lanes
+    Words u = __builtin_bit_cast(Words, x);
 #pragma unroll
     for (int i = 0; i < kWords; ++i) u.w[i] = __builtin_amdgcn_mov_dpp(u.w[i], 0x120 + decltype(n)::value, 0xF, 0xF, false);
     return __builtin_bit_cast(V, u);
   };
-  v = op(v, ror(v, std::integral_constant<int, 8>{}));  // row_ror within 16 lanes
+  v = op(v, ror(v, std::integral_constant<int, 8>{}));
   v = op(v, ror(v, std::integral_constant<int, 4>{}));
   v = op(v, ror(v, std::integral_constant<int, 2>{}));
   v = op(v, ror(v, std::integral_constant<int, 1>{}));
+  if constexpr (LANES >= 32) {  // the two rows of 16 of each half
+    Words a = __builtin_bit_cast(Words, v), b;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const u32x2 both = __builtin_amdgcn_permlane16_swap((unsigned)a.w[i], (unsigned)a.w[i], false, false);
+      a.w[i] = (int)both[0], b.w[i] = (int)both[1];
+    }
+    v = op(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b));
+  }
   if constexpr (LANES == 64) {
-    v = op(v, __shfl_xor(v, 16));
-    v = op(v, __shfl_xor(v, 32));
+    Words a = __builtin_bit_cast(Words, v), b;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const u32x2 both = __builtin_amdgcn_permlane32_swap((unsigned)a.w[i], (unsigned)a.w[i], false, false);
+      a.w[i] = (int)both[0], b.w[i] = (int)both[1];
+    }
+    v = op(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b));
   }
   return v;
 }
@@ -68,64 +85,21 @@ __device__ __forceinline__ float sigmoid_slope(float x) {
   return e / ((1.0f + e) * (1.0f + e));
 }
 
-// LANES lanes a token, V experts a lane (expert v LANES + lane).  The keys are the logits themselves, or with a bias
-// s + bias in 64 bits: two experts' keys may lie closer than 32 bits tell apart.  A slot a round: the largest key, then
-// the lowest expert that has it; the lane of that number keeps it.
-template <class T, int LANES, int V, bool BIAS>
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteParams p) {
-  typedef std::conditional_t<BIAS, double, float> Key;
+// e^x by the hardware's 2^x: to (|x| + 2) 2^-23 relative.
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
+
+// The topk largest keys of a token's LANES lanes, V a lane (expert v LANES + lane), a round each: the largest key, then
+// the lowest expert that has it, which lane k keeps.
+template <int LANES, int V, class Key>
+__device__ __forceinline__ int choose(Key (&key)[V], int topk) {
   constexpr Key kNone = -(Key)kInf;
   const int lane = threadIdx.x % LANES;
-  const int64_t token = (int64_t)blockIdx.x * (kRouteThreads / LANES) + threadIdx.x / LANES;
-  const bool ok = token < p.tokens;  // every lane takes part in the exchanges
-  const int64_t at = (ok ? token : 0) * p.num_experts;
-  const auto most = [](auto a, auto b) { return a > b ? a : b; };  // keys are never NaN here
-  const auto sum = [](auto a, auto b) { return a + b; };
-
-  Key key[V];
-  float top = 0.f, total = 1.f;  // softmax: the largest logit, sum of e^(l - top)
-  {
-    float l[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) l[v] = v * LANES + lane < p.num_experts ? load_logit<T>(p.logits, at + v * LANES + lane) : -kInf;
-    if (!p.sigmoid && (BIAS || !p.normalize)) {
-      float m = -kInf;
-#pragma unroll
-      for (int v = 0; v < V; ++v) m = fmaxf(m, l[v]);
-      m = lanes_all<LANES>(m, most);
-      top = m > -kInf ? m : 0.f;
-      float s = 0.f;
-#pragma unroll
-      for (int v = 0; v < V; ++v) s += expf(l[v] - top);
-      total = lanes_all<LANES>(s, sum);
-    }
-    if constexpr (BIAS) {
-      double sum64 = 1.0;
-      if (!p.sigmoid) {
-        sum64 = 0.0;
-#pragma unroll
-        for (int v = 0; v < V; ++v) sum64 += exp((double)l[v] - (double)top);
-        sum64 = lanes_all<LANES>(sum64, sum);
-      }
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = v * LANES + lane;
-        const double s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l[v])) : exp((double)l[v] - (double)top) / sum64;
-        const double k = l[v] > -kInf && e < p.num_experts ? s + (double)p.bias[e] : kNone;
-        key[v] = k > kNone ? k : kNone;  // NaN too
-      }
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) key[v] = l[v] > kNone ? l[v] : kNone;
-    }
-  }
-
   int mine = -1;
-  for (int k = 0; k < p.topk; ++k) {
+  for (int k = 0; k < topk; ++k) {
     Key best = key[0];
 #pragma unroll
-    for (int v = 1; v < V; ++v) best = most(best, key[v]);
-    best = lanes_all<LANES>(best, most);
+    for (int v = 1; v < V; ++v) best = best > key[v] ? best : key[v];  // keys are never NaN
+    best = lanes_all<LANES>(best, [](Key a, Key b) { return a > b ? a : b; });
     int e = kNoExpert;
 #pragma unroll
     for (int v = V - 1; v >= 0; --v) e = key[v] == best ? v * LANES + lane : e;
@@ -134,23 +108,169 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteParams p) {
     for (int v = 0; v < V; ++v) key[v] = v * LANES + lane == e ? kNone : key[v];
     if (lane == k) mine = best > kNone ? e : -1;
   }
+  return mine;
+}
 
-  const float l = mine >= 0 ? load_logit<T>(p.logits, at + mine) : -kInf;
+// The same of keys of 22 bits above 1023 - expert (0: none), so that one maximum finds key and expert (a round 44
+// instructions where `choose` takes 130, at V = 16).  `close`: whether two neighbours among the topk and the next one are
+// less than `near` apart in a token of the wave; the rounds then go on until the last chosen and the next one are not, so
+// that the experts that the lanes keep hold all that may belong to the topk.  false: not within LANES rounds.
+template <int LANES, int V>
+__device__ __forceinline__ bool choose_packed(uint32_t (&key)[V], int topk, uint32_t near, int& mine, bool& close) {
+  const int lane = threadIdx.x % LANES;
+  uint32_t before = 0;
+  mine = -1;
+  for (int k = 0;; ++k) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) best = max(best, key[v]);
+    best = lanes_all<LANES>(best, [](uint32_t a, uint32_t b) { return max(a, b); });
+    const bool next = k > 0 && best != 0 && (before >> 10) - (best >> 10) < near;
+    if (k <= topk) close |= __ballot(next) != 0;
+    if (k >= topk && __ballot(next) == 0) return true;
+    if (k == LANES) return false;
+    before = best;
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = key[v] == best ? 0 : key[v];
+    if (lane == k && best != 0) mine = 1023 - (int)(best & 1023);
+  }
+}
+
+// The place of the lane's expert among its LANES lanes' by their exact keys, equal ones by number; lanes without one keep
+// theirs (the last).
+template <int LANES, class Key>
+__device__ __forceinline__ int place_of(Key key, int e) {
+  const int lane = threadIdx.x % LANES, base = (threadIdx.x & 63) - lane;
+  int place = e < 0 ? lane : 0;
+#pragma unroll 4
+  for (int i = 0; i < LANES; ++i) {
+    const Key other = __shfl(key, base + i);
+    const int other_e = __shfl(e, base + i);
+    place += e >= 0 && other_e >= 0 && (other > key || (other == key && other_e < e));
+  }
+  return place;
+}
+
+// A logit of 16 bits as 16 bits that rise with it (both zeros one value).
+__device__ __forceinline__ uint32_t rising_bits(uint32_t h) {
+  h = h == 0x8000u ? 0u : h;
+  return (h & 0x8000u) ? 0xFFFFu - h : h | 0x8000u;
+}
+
+// The choice is made on keys of 22 bits.  Logits of 16 bits are whole in them, and equal keys are equal logits.  fp32
+// logits are compared by their distance from the largest, in steps of 2^-18, and sums with a bias in steps of 2^-20 (off
+// by less than 2^-18: the score by at most 48 roundings of 2^-24, the sum by two, the step); where two that matter are
+// not told apart by that (fp32: one step; sums: 9 steps), the candidates are put in order by the logits themselves or by
+// sums in 64 bits (two sums may lie closer than 32 bits tell apart); too many candidates: all experts are, the slow way,
+// whose waves a launch waits for.
+template <class T, int LANES, int V, bool BIAS>
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteParams p) {
+  constexpr bool kWhole = !BIAS && sizeof(T) == 2;
+  constexpr uint32_t kMostKey = (1u << 22) - 1;
+  const int lane = threadIdx.x % LANES;
+  const int64_t token = (int64_t)blockIdx.x * (kRouteThreads / LANES) + threadIdx.x / LANES;
+  const bool ok = token < p.tokens;  // every lane takes part in the exchanges
+  const int64_t at = (ok ? token : 0) * p.num_experts;
+  const auto sum = [](auto a, auto b) { return a + b; };
+  const auto most = [](float a, float b) { return fmaxf(a, b); };
+
+  float l[V];
+  uint32_t key[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) l[v] = load_logit<T>(p.logits, at + min(v * LANES + lane, p.num_experts - 1));
+  float bias[BIAS ? V : 1];
+  if constexpr (BIAS) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) bias[v] = p.bias[min(v * LANES + lane, p.num_experts - 1)];
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) l[v] = v * LANES + lane < p.num_experts ? l[v] : -kInf;
+  float top = 0.f, total = 1.f;  // the largest logit; softmax: sum of e^(l - top)
+  if (!kWhole || !(p.sigmoid || p.normalize)) {
+    float m = -kInf;
+#pragma unroll
+    for (int v = 0; v < V; ++v) m = fmaxf(m, l[v]);
+    m = lanes_all<LANES>(m, most);
+    top = m > -kInf ? m : 0.f;
+  }
+  if (!p.sigmoid && (BIAS || !p.normalize)) {
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) s += fast_exp(l[v] - top);
+    total = lanes_all<LANES>(s, sum);
+  }
+  bool close = false;
+  if constexpr (BIAS) {
+    float k[V];
+    if (p.sigmoid) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) k[v] = __builtin_amdgcn_rcpf(1.0f + fast_exp(-l[v])) + bias[v];
+    } else {
+      const float inv = 1.0f / total;
+#pragma unroll
+      for (int v = 0; v < V; ++v) k[v] = __builtin_fmaf(fast_exp(l[v] - top), inv, bias[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {  // -2 .. 2, what lies outside at the ends; NaN and -inf: left out
+      const float f = fminf(fmaxf(__builtin_fmaf(k[v], 0x1p20f, 0x1p21f), 1.f), (float)kMostKey);
+      key[v] = l[v] > -kInf && k[v] > -kInf ? (uint32_t)f << 10 | (1023 - (v * LANES + lane)) : 0u;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      uint32_t u;
+      if constexpr (kWhole) u = 1 + rising_bits(__builtin_bit_cast(uint16_t, from_float<T>(l[v])));
+      else u = (uint32_t)fminf(fmaxf((16.f - (top - l[v])) * 0x1p18f, 1.f), (float)kMostKey);
+      key[v] = l[v] > -kInf ? u << 10 | (1023 - (v * LANES + lane)) : 0u;
+    }
+    if constexpr (!kWhole) close = top == kInf;  // no distances
+  }
+  int mine, slot = lane;
+  const bool listed = choose_packed<LANES, V>(key, p.topk, kWhole ? 0u : BIAS ? 9u : 1u, mine, close);
+  if (!kWhole && close) {
+    double sum64 = 1.0;
+    if (BIAS && !p.sigmoid) {
+      sum64 = 0.0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) sum64 += exp((double)l[v] - (double)top);
+      sum64 = lanes_all<LANES>(sum64, sum);
+    }
+    const auto exact = [&](float x, float b) {
+      if constexpr (!BIAS) return x;
+      else return (p.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - (double)top) / sum64) + (double)b;
+    };
+    typedef std::conditional_t<BIAS, double, float> Key;
+    if (listed) {
+      const Key own = mine < 0 ? -(Key)kInf : exact(load_logit<T>(p.logits, at + mine), BIAS ? p.bias[mine] : 0.f);
+      slot = place_of<LANES>(own, mine);
+      if (slot >= p.topk) mine = -1;
+    } else {
+      Key all[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const Key k = exact(l[v], BIAS ? bias[v] : 0.f);
+        all[v] = l[v] > -kInf && k > -(Key)kInf ? k : -(Key)kInf;
+      }
+      mine = choose<LANES, V>(all, p.topk);
+    }
+  }
+
+  const float mine_l = mine >= 0 ? load_logit<T>(p.logits, at + mine) : -kInf;
   float w;
   if (p.sigmoid) {
-    w = mine >= 0 ? sigmoid_of(l) : 0.f;
+    w = mine >= 0 ? sigmoid_of(mine_l) : 0.f;
   } else {
     if (p.normalize) {
-      const float m = lanes_all<LANES>(l, [](float a, float b) { return fmaxf(a, b); });
+      const float m = lanes_all<LANES>(mine_l, most);
       top = m > -kInf ? m : 0.f;
     }
-    w = mine >= 0 ? expf(l - top) : 0.f;
+    w = mine >= 0 ? expf(mine_l - top) : 0.f;
   }
   if (p.normalize) total = lanes_all<LANES>(w, sum);
   if (p.normalize || !p.sigmoid) w = w == 0.f && total == 0.f ? 0.f : w / total;
-  if (ok && lane < p.topk) {
-    p.experts[token * p.topk + lane] = mine;
-    p.weights[token * p.topk + lane] = p.scale * w;
+  if (ok && slot < p.topk) {
+    p.experts[token * p.topk + slot] = mine;
+    p.weights[token * p.topk + slot] = p.scale * w;
   }
 }
 
@@ -277,34 +397,66 @@ __device__ __forceinline__ uint64_t same_lanes(int v, int bits) {
 }
 
 // The rows of a run's slots: the rows of smaller experts, of the expert's slots in earlier runs, in the run's earlier
-// parts and in the part before the slot.  Every workgroup adds up the counts it needs by itself.
+// parts and in the part before the slot.  Every workgroup adds up the counts it needs by itself.  ONE: a run of kSortRun
+// slots, whose experts stay in registers.
+template <bool ONE>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortParams p) {
+  constexpr int kMine = ONE ? kSortRun / kSortThreads : 1;  // slots of a lane
   __shared__ int part[kSortWaves][kMaxExperts];  // slots of a wave's part; then the next row of each expert in it
+  __shared__ int totals[kMaxExperts], befores[kMaxExperts];  // slots of an expert: in all, in earlier runs
   __shared__ int wave_sum[kSortWaves];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, E = p.num_experts;
   const int64_t begin = blockIdx.x * p.run, share = p.run / kSortWaves;
   const int64_t part_begin = begin + wave * share, part_end = min(part_begin + share, p.slots);
-  for (int e = threadIdx.x; e < kSortWaves * kMaxExperts; e += kSortThreads) part[0][e] = 0;
+  int mine[kMine];
+  if constexpr (ONE) {
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+      const int64_t i = part_begin + 64 * j + lane;
+      mine[j] = i < part_end ? p.experts[i] : -1;
+    }
+  }
+  for (int e = threadIdx.x; e < kSortWaves * kMaxExperts; e += kSortThreads) {
+    if (e % kMaxExperts < E) part[0][e] = 0;
+  }
+  for (int e = threadIdx.x; e < E; e += kSortThreads) totals[e] = befores[e] = 0;
   __syncthreads();
-  for (int64_t i = part_begin + lane; i < part_end; i += 64) {
-    const int e = p.experts[i];
-    if ((unsigned)e < (unsigned)p.num_experts) atomicAdd(&part[wave][e], 1);
+  if constexpr (ONE) {
+#pragma unroll
+    for (int j = 0; j < kMine; ++j)
+      if ((unsigned)mine[j] < (unsigned)E) atomicAdd(&part[wave][mine[j]], 1);
+  } else {
+    for (int64_t i = part_begin + lane; i < part_end; i += 64) {
+      const int e = p.experts[i];
+      if ((unsigned)e < (unsigned)E) atomicAdd(&part[wave][e], 1);
+    }
+  }
+  if (p.blocks > 1) {  // threads side by side take one run's experts, or a part of them
+    const int side = min(E, kSortThreads), lines = kSortThreads / side, line = threadIdx.x / side;
+    for (int e = threadIdx.x % side; line < lines && e < E; e += side) {
+      int all = 0, before = 0;
+#pragma unroll 8
+      for (int b = line; b < p.blocks; b += lines) {
+        const int c = p.counts[(int64_t)b * E + e];
+        all += c;
+        before += b < (int)blockIdx.x ? c : 0;
+      }
+      atomicAdd(&totals[e], all);
+      atomicAdd(&befores[e], before);
+    }
   }
   __syncthreads();
   // two experts a thread: 2 t, 2 t + 1
-  int total[2] = {0, 0}, before[2] = {0, 0};
+  int total[2] = {0, 0};
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int e = 2 * threadIdx.x + j;
-    if (e >= p.num_experts) continue;
-    if (p.blocks == 1) {
-      for (int w = 0; w < kSortWaves; ++w) total[j] += part[w][e];
+    if (e >= E) continue;
+    if (p.blocks > 1) {
+      total[j] = totals[e];
     } else {
-      for (int b = 0; b < p.blocks; ++b) {
-        const int c = p.counts[(int64_t)b * p.num_experts + e];
-        total[j] += c;
-        before[j] += b < (int)blockIdx.x ? c : 0;
-      }
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) total[j] += part[w][e];
     }
   }
   // rows of the smaller experts: a scan over the threads
@@ -317,6 +469,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortParams p) 
   if (lane == 63) wave_sum[wave] = scan;
   __syncthreads();
   int rows = 0, first = scan - total[0] - total[1];
+#pragma unroll
   for (int w = 0; w < kSortWaves; ++w) {
     first += w < wave ? wave_sum[w] : 0;
     rows += wave_sum[w];
@@ -324,9 +477,10 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortParams p) 
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int e = 2 * threadIdx.x + j;
-    if (e >= p.num_experts) continue;
+    if (e >= E) continue;
     if (blockIdx.x == 0) p.m_splits[e] = total[j];
-    int row = first + (j == 1 ? total[0] : 0) + before[j];
+    int row = first + (j == 1 ? total[0] : 0) + befores[e];
+#pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
       const int n = part[w][e];
       part[w][e] = row;
@@ -335,12 +489,10 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortParams p) 
   }
   __syncthreads();
   int bits = 1;
-  while ((1 << bits) <= p.num_experts) ++bits;  // the experts and one more value
-  for (int64_t i0 = part_begin; i0 < part_end; i0 += 64) {
-    const int64_t i = i0 + lane;
-    int e = i < part_end ? p.experts[i] : -1;
-    const bool valid = (unsigned)e < (unsigned)p.num_experts;
-    e = valid ? e : p.num_experts;
+  while ((1 << bits) <= E) ++bits;  // the experts and one more value
+  const auto place = [&](int64_t i, int e) {
+    const bool valid = (unsigned)e < (unsigned)E;
+    e = valid ? e : E;
     const uint64_t same = same_lanes(e, bits);
     const int rank = __popcll(same & ((1ull << lane) - 1));
     int row = -1;
@@ -352,6 +504,13 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortParams p) 
     if (valid && rank == 0) part[wave][e] = row + __popcll(same);
     if (i < part_end) p.row_of[i] = row;
     __builtin_amdgcn_wave_barrier();
+  };
+  if constexpr (ONE) {
+#pragma unroll
+    for (int j = 0; j < kMine; ++j)
+      if (part_begin + 64 * j < part_end) place(part_begin + 64 * j + lane, mine[j]);
+  } else {
+    for (int64_t i0 = part_begin; i0 < part_end; i0 += 64) place(i0 + lane, i0 + lane < part_end ? p.experts[i0 + lane] : -1);
   }
   for (int64_t r = begin + threadIdx.x; r < min(begin + p.run, p.slots); r += kSortThreads)
     if (r >= rows) p.slot_of[r] = -1;
@@ -461,6 +620,7 @@ extern "C" te_status te_moe_sort(const int32_t* experts, int64_t slots, int32_t 
     const te_status st = launch_status();
     if (st != TE_OK) return st;
   }
-  hipLaunchKernelGGL(sort_place_kernel, dim3(blocks), dim3(kSortThreads), 0, stream, p);
+  if (p.run == kSortRun) hipLaunchKernelGGL((sort_place_kernel<true>), dim3(blocks), dim3(kSortThreads), 0, stream, p);
+  else hipLaunchKernelGGL((sort_place_kernel<false>), dim3(blocks), dim3(kSortThreads), 0, stream, p);
   return launch_status();
 }
