@@ -113,6 +113,7 @@ for _name, (_res, _args) in _SIGS.items():
     _fn.argtypes = _args
 
 EXPORTED = tuple(_SIGS)
+_FNS = {_name: getattr(_lib, _name) for _name in _SIGS}
 
 
 class TemxError(RuntimeError):
@@ -439,6 +440,11 @@ except ImportError:
     def _current_stream(index):
         return torch.cuda.current_stream(index).cuda_stream
 
+try:  # the current device's index without the check that the GPU is in use (0.2 us)
+    from torch._C import _cuda_getDevice as _current_device
+except ImportError:
+    _current_device = torch.cuda.current_device
+
 _FLOATS = "bfloat16, float16 or float32"
 _CODES = "1-byte codes (uint8)"
 _B16 = "bf16 (or its int16 bits)"
@@ -452,6 +458,8 @@ def _addr(t, name, shape, kind, index):
     first tensor's, -1 on the CPU)."""
     if t is None:
         raise ValueError(f"{name} is required")
+    if t.shape == shape and t.dtype in _KINDS[kind] and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype not in _KINDS[kind]:
         raise ValueError(f"{name}: expected {kind}, got {t.dtype}")
     if t.shape != shape:
@@ -489,11 +497,11 @@ def _run(name, args, index, stream):
     if index < 0:
         raise ValueError("expected a GPU tensor, got one on the CPU")
     handle = _current_stream(index) if stream is None else _stream(stream)
-    if index == torch.cuda.current_device():
-        status = getattr(_lib, name)(*args, handle)
+    if index == _current_device():
+        status = _FNS[name](*args, handle)
     else:
         with torch.cuda.device(index):
-            status = getattr(_lib, name)(*args, handle)
+            status = _FNS[name](*args, handle)
     if status != TE_OK:
         raise TemxError(name, status)
 
@@ -631,28 +639,31 @@ def _score(score) -> int:
 def _route_args(score, logits, experts):
     """(device index, score, logits' address and dtype, tokens, experts in all, topk, experts' address)"""
     index = _index_of(logits, "logits")
-    _require(logits.dtype in _NORM_DTYPES, f"logits: expected {_FLOATS}, got {logits.dtype}")
-    _require(experts is not None and experts.dim() == 2, "experts: expected a 2-D int32 tensor")
-    tokens, n = logits.shape
+    dt = _NORM_DTYPES.get(logits.dtype)
+    if dt is None:
+        raise ValueError(f"logits: expected {_FLOATS}, got {logits.dtype}")
+    if experts is None or experts.dim() != 2:
+        raise ValueError("experts: expected a 2-D int32 tensor")
+    tokens, n = shape = logits.shape
     topk = experts.shape[1]
-    return (index, _score(score), _addr(logits, "logits", (tokens, n), logits.dtype, index), _NORM_DTYPES[logits.dtype],
-            tokens, n, topk, _addr(experts, "experts", (tokens, topk), "int32", index))
+    return (index, _score(score), _addr(logits, "logits", shape, logits.dtype, index), dt, tokens, n, topk,
+            _addr(experts, "experts", (tokens, topk), "int32", index))
 
 
 def te_moe_route(score, logits, experts, weights, bias=None, normalize=True, scale=1.0, stream=None) -> None:
     """experts int32 [tokens, topk] and weights float32 [tokens, topk] are written."""
     i, score, logits_at, dt, tokens, n, topk, experts_at = _route_args(score, logits, experts)
     _run("te_moe_route", (
-        score, logits_at, dt, tokens, n, topk, _opt(bias, "bias", (n,), "float32", i), int(bool(normalize)), scale,
-        experts_at, _addr(weights, "weights", (tokens, topk), "float32", i)), i, stream)
+        score, logits_at, dt, tokens, n, topk, None if bias is None else _addr(bias, "bias", (n,), "float32", i),
+        1 if normalize else 0, scale, experts_at, _addr(weights, "weights", (tokens, topk), "float32", i)), i, stream)
 
 
 def te_moe_route_backward(score, logits, experts, dweights, dlogits, normalize=True, scale=1.0, stream=None) -> None:
     i, score, logits_at, dt, tokens, n, topk, experts_at = _route_args(score, logits, experts)
     _run("te_moe_route_backward", (
-        score, logits_at, dt, tokens, n, topk, int(bool(normalize)), scale, experts_at,
+        score, logits_at, dt, tokens, n, topk, 1 if normalize else 0, scale, experts_at,
         _addr(dweights, "dweights", (tokens, topk), "float32", i),
-        _addr(dlogits, "dlogits", (tokens, n), logits.dtype, i)), i, stream)
+        _addr(dlogits, "dlogits", logits.shape, logits.dtype, i)), i, stream)
 
 
 def te_moe_sort_workspace_size(slots: int, num_experts: int) -> int:
@@ -672,56 +683,69 @@ def te_moe_sort(experts, m_splits, row_of, slot_of, workspace=None, stream=None)
 
 def _rows_args(row_of, tokens, index):
     """(topk, address) of row_of [tokens, topk]."""
-    _require(row_of is not None and row_of.dim() == 2, "row_of: expected a 2-D int32 tensor")
+    if row_of is None or row_of.dim() != 2:
+        raise ValueError("row_of: expected a 2-D int32 tensor")
     topk = row_of.shape[1]
     return topk, _addr(row_of, "row_of", (tokens, topk), "int32", index)
 
 
 def _rows_out(y, q, q_scale, dtype, cols, index, name):
     """(rows in all, addresses of y, q and q_scale) of the outputs with a row each slot."""
-    _require(y is not None or q is not None, f"{name} or q is required")
     first = y if y is not None else q
-    _require(first.dim() == 2, f"{name}: expected a 2-D tensor")
+    if first is None:
+        raise ValueError(f"{name} or q is required")
+    if first.dim() != 2:
+        raise ValueError(f"{name}: expected a 2-D tensor")
     rows = first.shape[0]
-    if q is not None:
-        _require(cols % 32 == 0, "q: the MXFP8 output needs cols % 32 == 0")
-    return (rows, _opt(y, name, (rows, cols), dtype, index), _opt(q, "q", (rows, cols), _CODES, index),
-            _opt(q_scale, "q_scale", (rows, cols // 32), _CODES, index))
+    if q is None:
+        if q_scale is not None:
+            raise ValueError("q_scale: only with q")
+        return rows, _addr(y, name, (rows, cols), dtype, index), None, None
+    if cols % 32 != 0:
+        raise ValueError("q: the MXFP8 output needs cols % 32 == 0")
+    return (rows, _opt(y, name, (rows, cols), dtype, index), _addr(q, "q", (rows, cols), _CODES, index),
+            _addr(q_scale, "q_scale", (rows, cols // 32), _CODES, index))
 
 
 def _float_2d(t, name):
+    """(device index, dtype, its code, shape) of a 2-D tensor of floats."""
     index = _index_of(t, name)
-    _require(t.dtype in _NORM_DTYPES, f"{name}: expected {_FLOATS}, got {t.dtype}")
-    return index, t.dtype, t.shape
+    dt = _NORM_DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name}: expected {_FLOATS}, got {t.dtype}")
+    return index, t.dtype, dt, t.shape
 
 
 def te_moe_dispatch(x, row_of, y=None, q=None, q_scale=None, q_fmt="e4m3", stream=None) -> None:
-    i, xd, (tokens, cols) = _float_2d(x, "x")
+    i, xd, dt, shape = _float_2d(x, "x")
+    tokens, cols = shape
     topk, row_at = _rows_args(row_of, tokens, i)
     rows, py, pq, pqs = _rows_out(y, q, q_scale, xd, cols, i, "y")
-    _run("te_moe_dispatch", (_addr(x, "x", (tokens, cols), xd, i), _NORM_DTYPES[xd], tokens, cols, row_at, topk, rows,
-                             py, pq, pqs, _fmt(q_fmt)), i, stream)
+    _run("te_moe_dispatch", (_addr(x, "x", shape, xd, i), dt, tokens, cols, row_at, topk, rows, py, pq, pqs,
+                             _fmt(q_fmt)), i, stream)
 
 
 def te_moe_combine(rows, row_of, y, weights=None, stream=None) -> None:
     """weights None: all 1, the gradient of te_moe_dispatch."""
-    i, xd, (total, cols) = _float_2d(rows, "rows")
+    i, xd, dt, shape = _float_2d(rows, "rows")
+    total, cols = shape
     _require(y is not None and y.dim() == 2, "y: expected a 2-D tensor")
     tokens = y.shape[0]
     topk, row_at = _rows_args(row_of, tokens, i)
-    _run("te_moe_combine", (_addr(rows, "rows", (total, cols), xd, i), _NORM_DTYPES[xd], total, cols, row_at,
+    _run("te_moe_combine", (_addr(rows, "rows", shape, xd, i), dt, total, cols, row_at,
                             _opt(weights, "weights", (tokens, topk), "float32", i), tokens, topk,
                             _addr(y, "y", (tokens, cols), xd, i)), i, stream)
 
 
 def te_moe_combine_backward(dy, rows, row_of, weights, dweights, drows=None, q=None, q_scale=None, q_fmt="e5m2",
                             stream=None) -> None:
-    i, xd, (tokens, cols) = _float_2d(dy, "dy")
+    i, xd, dt, shape = _float_2d(dy, "dy")
+    tokens, cols = shape
     topk, row_at = _rows_args(row_of, tokens, i)
     total, pd, pq, pqs = _rows_out(drows, q, q_scale, xd, cols, i, "drows")
     _run("te_moe_combine_backward", (
-        _addr(dy, "dy", (tokens, cols), xd, i), _addr(rows, "rows", (total, cols), xd, i), _NORM_DTYPES[xd], tokens,
-        cols, row_at, _addr(weights, "weights", (tokens, topk), "float32", i), topk, total, pd, pq, pqs, _fmt(q_fmt),
+        _addr(dy, "dy", shape, xd, i), _addr(rows, "rows", (total, cols), xd, i), dt, tokens, cols, row_at,
+        _addr(weights, "weights", (tokens, topk), "float32", i), topk, total, pd, pq, pqs, _fmt(q_fmt),
         _addr(dweights, "dweights", (tokens, topk), "float32", i)), i, stream)
 
 
@@ -735,28 +759,33 @@ _KINDS["a scale type"] = frozenset(_W4_SCALES)
 def _w4_args(x, w, w_fmt, w_scale, zero, rows, d, n):
     """(device index, the arguments up to the group size, M, K, d's address and dtype) of rows x K weights."""
     i = _index_of(x, "x")
-    _require(x.dtype in (torch.bfloat16, torch.float16), f"x: expected bfloat16 or float16, got {x.dtype}")
-    M, K = x.shape
-    _require(w_scale is not None and w_scale.dim() == 2, "w_scale must be 2-D")
+    xd = x.dtype
+    if xd is not torch.bfloat16 and xd is not torch.float16:
+        raise ValueError(f"x: expected bfloat16 or float16, got {xd}")
+    M, K = shape = x.shape
+    if w_scale is None or w_scale.dim() != 2:
+        raise ValueError("w_scale must be 2-D")
     scales = w_scale.shape[1]
-    _require(scales > 0 and K % scales == 0 if K else scales == 0,
-             f"w_scale: {scales} columns do not divide K = {K} into groups")
-    dt = _NORM_DTYPES[x.dtype]
+    if K % 2 != 0 or (K % scales != 0 if scales else K != 0):
+        raise ValueError(f"w_scale: {scales} columns do not divide K = {K} into groups")
+    dt = _NORM_DTYPES[xd]
     scale_dt = _W4_SCALES.get(w_scale.dtype)
-    _require(scale_dt is not None and (scale_dt != TE_BF16 and scale_dt != TE_FP16 or scale_dt == dt),
-             f"w_scale: expected x's dtype, float32 or E8M0 codes (uint8), got {w_scale.dtype}")
-    _require(d is not None and (d.dtype == x.dtype or d.dtype == torch.float32), "d: expected x's dtype or float32")
-    _require(K % 2 == 0, "w: K must be even (two codes a byte)")
-    args = (_addr(x, "x", (M, K), x.dtype, i), dt, _addr(w, "w", (rows, K // 2), _CODES, i),
+    if scale_dt is None or (scale_dt != dt and scale_dt != TE_FP32 and scale_dt != TE_E8M0):
+        raise ValueError(f"w_scale: expected x's dtype, float32 or E8M0 codes (uint8), got {w_scale.dtype}")
+    if d is None or (d.dtype != xd and d.dtype != torch.float32):
+        raise ValueError("d: expected x's dtype or float32")
+    args = (_addr(x, "x", shape, xd, i), dt, _addr(w, "w", (rows, K // 2), _CODES, i),
             W4_FORMATS[w_fmt] if isinstance(w_fmt, str) else int(w_fmt),
             _addr(w_scale, "w_scale", (rows, scales), "a scale type", i), scale_dt,
-            _opt(zero, "zero", (rows, scales), _CODES, i), K // scales if scales else 32)
+            None if zero is None else _addr(zero, "zero", (rows, scales), _CODES, i), K // scales if scales else 32)
     return i, args, M, K, _addr(d, "d", (M, n), d.dtype, i), _NORM_DTYPES[d.dtype]
 
 
 def _rows_of(t, name, per=1):
-    _require(t is not None and t.dim() == 2, f"{name} must be 2-D")
-    _require(t.shape[0] % per == 0, f"{name}: expected an even number of rows (gate rows, then up rows)")
+    if t is None or t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if t.shape[0] % per != 0:
+        raise ValueError(f"{name}: expected an even number of rows (gate rows, then up rows)")
     return t.shape[0] // per
 
 

@@ -24,14 +24,52 @@ struct RowsParams {
   bool q_e5m2;
 };
 
-// The row of a slot, -1 where it has none (or one outside the tensor).
-__device__ __forceinline__ int64_t row_at(const RowsParams& p, int64_t slot) {
-  const int r = p.row_of[slot];
-  return r >= 0 && r < p.total_rows ? r : -1;
+// The rows of kSlots slots of a token from slot k on, -1 where there is none (or one outside the tensor): loaded together,
+// ahead of the accesses that need them.
+constexpr int kSlots = 4;
+__device__ __forceinline__ void rows_at(const RowsParams& p, int64_t token, int k, int64_t (&rows)[kSlots]) {
+  int r[kSlots];
+#pragma unroll
+  for (int j = 0; j < kSlots; ++j) r[j] = p.row_of[token * p.topk + min(k + j, p.topk - 1)];
+#pragma unroll
+  for (int j = 0; j < kSlots; ++j) rows[j] = k + j < p.topk && r[j] >= 0 && r[j] < p.total_rows ? r[j] : -1;
+}
+
+// Whole chunks past the caches where STREAM (see streams()).
+template <class T, bool STREAM>
+__device__ __forceinline__ void put_chunk(T* p, const Raw<T>& r, int n) {
+  if (!STREAM || n < kChunk) return store_chunk(p, r, n);
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(r.w) / 16; ++i)
+    __builtin_nontemporal_store(u32x4{r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]},
+                                reinterpret_cast<typename Vec16<sizeof(T)>::type*>(p) + i);
+}
+
+// load_ahead, past the caches where STREAM.  (With load_ahead's own load of a whole chunk beside it the compiler makes one
+// load of both, without the hint.)
+template <class T, bool STREAM>
+__device__ __forceinline__ Raw<T> get_ahead(const T* row, int c, int n) {
+  if constexpr (!STREAM) return load_ahead(row, c, n);
+  Raw<T> r;
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(r.w) / 4; ++i) r.w[i] = 0;
+  if (n >= kChunk) {
+    if (c < n) {
+#pragma unroll
+      for (unsigned i = 0; i < sizeof(r.w) / 16; ++i) {
+        const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const typename Vec16<sizeof(T)>::type*>(row + min(c, n - kChunk)) + i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r.w[4 * i + e] = v[e];
+      }
+    }
+  } else {
+    r = load_ahead(row, c, n);
+  }
+  return r;
 }
 
 // A thread takes one chunk of a token: read once, written to each of its rows.
-template <class T>
+template <class T, bool STREAM>
 __global__ __launch_bounds__(kThreads) void dispatch_kernel(RowsParams p, int chunks) {
   const int64_t i = (p.block0 + blockIdx.x) * kThreads + threadIdx.x;
   const int64_t token = i / chunks;
@@ -49,22 +87,27 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(RowsParams p, int ch
       codes = p.q_e5m2 ? cvt8_scaled<TE_E5M2>(bits, scale) : cvt8_scaled<TE_E4M3>(bits, scale);
     }
   }
-  for (int k = 0; k < p.topk; ++k) {
-    const int64_t r = row_at(p, token * p.topk + k);
-    if (r < 0) continue;
-    const int64_t at = r * p.cols + c;
-    if (p.y != nullptr) store_chunk(static_cast<T*>(p.y) + at, v, p.cols - c);
-    if constexpr (std::is_same_v<T, bf16_t>) {
-      if (p.q != nullptr) {
-        *reinterpret_cast<uint2*>(p.q + at) = codes;
-        if ((c & 31) == 0) p.q_scale[at >> 5] = (uint8_t)code;
+  for (int k = 0; k < p.topk; k += kSlots) {
+    int64_t rows[kSlots];
+    rows_at(p, token, k, rows);
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      if (rows[j] < 0) continue;
+      const int64_t at = rows[j] * p.cols + c;
+      if (p.y != nullptr) put_chunk<T, STREAM>(static_cast<T*>(p.y) + at, v, p.cols - c);
+      if constexpr (std::is_same_v<T, bf16_t>) {
+        if (p.q != nullptr) {
+          if (STREAM) store_nt8(p.q + at, codes);
+          else *reinterpret_cast<uint2*>(p.q + at) = codes;
+          if ((c & 31) == 0) p.q_scale[at >> 5] = (uint8_t)code;
+        }
       }
     }
   }
 }
 
 // A thread takes one chunk of a token: its rows' chunks added up in fp32 in the order of the slots, rounded once.
-template <class T>
+template <class T, bool STREAM>
 __global__ __launch_bounds__(kThreads) void combine_kernel(RowsParams p, int chunks) {
   const int64_t i = (p.block0 + blockIdx.x) * kThreads + threadIdx.x;
   const int64_t token = i / chunks;
@@ -73,33 +116,50 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(RowsParams p, int chu
   float sum[kChunk];
 #pragma unroll
   for (int e = 0; e < kChunk; ++e) sum[e] = 0.f;
-  for (int k = 0; k < p.topk; ++k) {
-    const int64_t slot = token * p.topk + k, r = row_at(p, slot);
-    if (r < 0) continue;
-    const float w = p.weights != nullptr ? p.weights[slot] : 1.f;
-    float f[kChunk];
-    load_floats(static_cast<const T*>(p.rows) + r * p.cols, c, p.cols, f);
+  for (int k = 0; k < p.topk; k += kSlots) {
+    int64_t rows[kSlots];
+    rows_at(p, token, k, rows);
+    float w[kSlots];
+    Raw<T> raw[kSlots];
 #pragma unroll
-    for (int e = 0; e < kChunk; ++e) sum[e] = __builtin_fmaf(w, f[e], sum[e]);
+    for (int j = 0; j < kSlots; ++j) {
+      w[j] = p.weights != nullptr && rows[j] >= 0 ? p.weights[token * p.topk + k + j] : 1.f;
+      if (rows[j] >= 0) raw[j] = get_ahead<T, STREAM>(static_cast<const T*>(p.rows) + rows[j] * p.cols, c, p.cols);
+    }
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      if (rows[j] < 0) continue;
+      float f[kChunk];
+      settle<T>(raw[j], c, p.cols);
+      unpack<T>(raw[j], f);
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) sum[e] = __builtin_fmaf(w[j], f[e], sum[e]);
+    }
   }
   store_chunk(static_cast<T*>(p.y) + token * p.cols + c, pack<T>(sum), p.cols - c);
 }
 
 // A wave takes one slot: w dy to its row and the dot product of dy with the experts' output there.
-template <class T>
+template <class T, bool STREAM>
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(RowsParams p) {
   const int lane = threadIdx.x & 63;
   const int64_t slot = (p.block0 + blockIdx.x) * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (slot >= p.tokens * p.topk) return;
-  const int64_t token = slot / p.topk, r = row_at(p, slot);
+  const int64_t token = slot / p.topk;
+  const int row = p.row_of[slot];
+  const int64_t r = row < p.total_rows ? row : -1;
   float dot = 0.f;
   if (r >= 0) {
     const float w = p.weights[slot];
-    const int cols_up = (p.cols + 64 * kChunk - 1) / (64 * kChunk) * (64 * kChunk);
-    for (int c = lane * kChunk; c < cols_up; c += 64 * kChunk) {  // every lane takes part in the quads' exchanges
+    const T* dy = static_cast<const T*>(p.x) + token * p.cols;
+    const T* out = static_cast<const T*>(p.rows) + r * p.cols;
+        for (int c0 = 0; c0 < p.cols; c0 += 64 * kChunk) {  // every lane takes part in the quads' exchanges
+      const int c = c0 + lane * kChunk;
       float g[kChunk], f[kChunk];
-      load_floats(static_cast<const T*>(p.x) + token * p.cols, c, p.cols, g);
-      load_floats(static_cast<const T*>(p.rows) + r * p.cols, c, p.cols, f);
+      load_floats(dy, c, p.cols, g);
+      Raw<T> raw = get_ahead<T, STREAM>(out, c, p.cols);
+      settle<T>(raw, c, p.cols);
+      unpack<T>(raw, f);
 #pragma unroll
       for (int e = 0; e < kChunk; ++e) {
         dot = __builtin_fmaf(g[e], f[e], dot);
@@ -107,7 +167,7 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(RowsParams p
       }
       const Raw<T> v = pack<T>(g);
       const int64_t at = r * p.cols + c;
-      if (p.y != nullptr) store_chunk(static_cast<T*>(p.y) + at, v, p.cols - c);
+      if (p.y != nullptr) put_chunk<T, STREAM>(static_cast<T*>(p.y) + at, v, p.cols - c);
       if constexpr (std::is_same_v<T, bf16_t>) {
         if (p.q != nullptr) store_mx(v, p.q, p.q_scale, at, c < p.cols, p.q_e5m2);
       }
@@ -133,11 +193,20 @@ te_status in_parts(RowsParams p, int64_t blocks, Launch launch) {
   return TE_OK;
 }
 
+// Whether the experts' rows pass the caches: above 96 MB.  Within them they may wait there for whoever takes them next,
+// and came from there (us a combine, calls in a stream on inputs in turn: 83 MB of rows 18.4 and 21.7 past the caches,
+// 134 MB 39.2 and 34.4; both read from cold caches 35 and 22, 62 and 37).
+template <class T>
+bool streams(const RowsParams& p) {
+  return p.tokens * p.topk * (int64_t)p.cols * (int64_t)sizeof(T) > (int64_t)96 << 20;
+}
+
 template <class T>
 te_status run_dispatch(const RowsParams& p, hipStream_t stream) {
   const int chunks = (p.cols + kChunk - 1) / kChunk;
   return in_parts(p, (p.tokens * chunks + kThreads - 1) / kThreads, [&](const RowsParams& q, dim3 grid) {
-    hipLaunchKernelGGL((dispatch_kernel<T>), grid, dim3(kThreads), 0, stream, q, chunks);
+    if (streams<T>(q)) hipLaunchKernelGGL((dispatch_kernel<T, true>), grid, dim3(kThreads), 0, stream, q, chunks);
+    else hipLaunchKernelGGL((dispatch_kernel<T, false>), grid, dim3(kThreads), 0, stream, q, chunks);
   });
 }
 
@@ -145,7 +214,8 @@ template <class T>
 te_status run_combine(const RowsParams& p, hipStream_t stream) {
   const int chunks = (p.cols + kChunk - 1) / kChunk;
   return in_parts(p, (p.tokens * chunks + kThreads - 1) / kThreads, [&](const RowsParams& q, dim3 grid) {
-    hipLaunchKernelGGL((combine_kernel<T>), grid, dim3(kThreads), 0, stream, q, chunks);
+    if (streams<T>(q)) hipLaunchKernelGGL((combine_kernel<T, true>), grid, dim3(kThreads), 0, stream, q, chunks);
+    else hipLaunchKernelGGL((combine_kernel<T, false>), grid, dim3(kThreads), 0, stream, q, chunks);
   });
 }
 
@@ -153,7 +223,8 @@ template <class T>
 te_status run_combine_backward(const RowsParams& p, hipStream_t stream) {
   const int64_t per = kThreads / 64;
   return in_parts(p, (p.tokens * p.topk + per - 1) / per, [&](const RowsParams& q, dim3 grid) {
-    hipLaunchKernelGGL((combine_backward_kernel<T>), grid, dim3(kThreads), 0, stream, q);
+    if (streams<T>(q)) hipLaunchKernelGGL((combine_backward_kernel<T, true>), grid, dim3(kThreads), 0, stream, q);
+    else hipLaunchKernelGGL((combine_backward_kernel<T, false>), grid, dim3(kThreads), 0, stream, q);
   });
 }
 
