@@ -667,7 +667,7 @@ te_status te_moe_combine(const void* rows, te_dtype dtype, int64_t total_rows, i
  *   dy       dtype [tokens, cols]; rows dtype [total_rows, cols]: what the
  *            forward combined
  *   drows    dtype [total_rows, cols], NULL where q is given; rows of no slot
- *            stay as they were
+ *            stay as they were.  drows may be rows itself.
  *   q, q_scale both or neither: drows as MXFP8 operand, as te_moe_dispatch's
  *   dweights float [tokens, topk]
  *   The rest as te_moe_dispatch.
