@@ -563,11 +563,17 @@ te_status w4_by_group(const W4Params& p, hipStream_t stream) {
 }
 
 template <class T, te_w4_format FMT, int NF>
-te_status w4_by_rows(const W4Params& p, int64_t rows, bool many, hipStream_t stream) {
-  if (rows <= 1) return many ? w4_by_group<T, FMT, W4Few<2, NF, 1, 2>>(p, stream) : w4_by_group<T, FMT, W4Few<8, NF, 1, 4>>(p, stream);
-  if (rows <= 4) return many ? w4_by_group<T, FMT, W4Few<4, NF, 4, 2>>(p, stream) : w4_by_group<T, FMT, W4Few<8, NF, 4, 4>>(p, stream);
-  if (rows <= 16) return w4_by_group<T, FMT, W4Ring<8, NF, 16, 3>>(p, stream);
-  return w4_by_group<T, FMT, W4Ring<7, NF, 32, 2>>(p, stream);
+te_status w4_by_rows(const W4Params& p, int64_t rows, int64_t tiles, hipStream_t stream) {
+  const int64_t cus = device_cu_count();
+  const bool many = tiles >= 3 * cus, ring_many = 2 * tiles * (p.m_splits != nullptr ? 1 : (p.M + 31) / 32) > 3 * cus;
+  if (rows <= 1) return many ? w4_by_group<T, FMT, W4Few<2, NF, 1, 2>>(p, stream) : w4_by_group<T, FMT, W4Few<8, NF, 1, 2>>(p, stream);
+  if (rows <= 4) {
+    if (many && p.K <= 2048) return w4_by_group<T, FMT, W4Few<2, NF, 4, 2, 16>>(p, stream);
+    if (!many && p.K >= 8192) return w4_by_group<T, FMT, W4Few<8, NF, 4, 2>>(p, stream);
+    return w4_by_group<T, FMT, W4Few<4, NF, 4, 2>>(p, stream);
+  }
+  if (rows <= 16) return ring_many ? w4_by_group<T, FMT, W4Ring<4, NF, 16, 2>>(p, stream) : w4_by_group<T, FMT, W4Ring<8, NF, 16, 3>>(p, stream);
+  return ring_many ? w4_by_group<T, FMT, W4Ring<3, NF, 32, 2>>(p, stream) : w4_by_group<T, FMT, W4Ring<7, NF, 32, 2>>(p, stream);
 }
 
 template <class T, te_w4_format FMT>
@@ -577,11 +583,11 @@ te_status w4_run(W4Params p, hipStream_t stream) {
   p.group_magic = (((uint64_t)1 << 40) + p.blocks_of_group - 1) / p.blocks_of_group;
   const bool grouped = p.m_splits != nullptr;
   // rows of a tile: all, or those of an expert on average and one more
-  const int64_t rows = grouped ? p.M / p.groups + 1 : p.M, experts = grouped ? p.groups : 1;
-  const int64_t tiles = (p.N + 15) / 16 * experts, enough = 3 * (int64_t)device_cu_count();
-  if (p.act >= 0) return w4_by_rows<T, FMT, 2>(p, rows, tiles >= enough, stream);
-  if (tiles >= 2 * enough) return w4_by_rows<T, FMT, 2>(p, rows, true, stream);
-  return w4_by_rows<T, FMT, 1>(p, rows, tiles >= enough, stream);
+  const int64_t rows = grouped ? p.M / p.groups + 1 : p.M, experts = grouped ? std::min<int64_t>(p.groups, p.M) : 1;
+  const int64_t tiles = (p.N + 15) / 16 * experts;
+  if (p.act >= 0) return w4_by_rows<T, FMT, 2>(p, rows, tiles, stream);
+  if (tiles >= 6 * (int64_t)device_cu_count()) return w4_by_rows<T, FMT, 2>(p, rows, tiles / 2, stream);
+  return w4_by_rows<T, FMT, 1>(p, rows, tiles, stream);
 }
 
 }  // namespace
