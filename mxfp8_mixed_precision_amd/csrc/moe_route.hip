@@ -33,44 +33,6 @@ struct RouteParams {
   bool sigmoid, normalize;
 };
 
-// op over the values of the lane's LANES (16, 32 or 64) lanes, in every lane.
-template <int LANES, class V, class Op>
-__device__ __forceinline__ V lanes_all(V v, Op op) {
-  constexpr int kWords = sizeof(V) / 4;
-  struct Words {
-    int w[kWords];
-  };
-  const auto ror = [](V x, auto n) {  // row_ror within 16 lanes
-    Words u = __builtin_bit_cast(Words, x);
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) u.w[i] = __builtin_amdgcn_mov_dpp(u.w[i], 0x120 + decltype(n)::value, 0xF, 0xF, false);
-    return __builtin_bit_cast(V, u);
-  };
-  v = op(v, ror(v, std::integral_constant<int, 8>{}));
-  v = op(v, ror(v, std::integral_constant<int, 4>{}));
-  v = op(v, ror(v, std::integral_constant<int, 2>{}));
-  v = op(v, ror(v, std::integral_constant<int, 1>{}));
-  if constexpr (LANES >= 32) {  // the two rows of 16 of each half
-    Words a = __builtin_bit_cast(Words, v), b;
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      const u32x2 both = __builtin_amdgcn_permlane16_swap((unsigned)a.w[i], (unsigned)a.w[i], false, false);
-      a.w[i] = (int)both[0], b.w[i] = (int)both[1];
-    }
-    v = op(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b));
-  }
-  if constexpr (LANES == 64) {
-    Words a = __builtin_bit_cast(Words, v), b;
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      const u32x2 both = __builtin_amdgcn_permlane32_swap((unsigned)a.w[i], (unsigned)a.w[i], false, false);
-      a.w[i] = (int)both[0], b.w[i] = (int)both[1];
-    }
-    v = op(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b));
-  }
-  return v;
-}
-
 template <class T>
 __device__ __forceinline__ float load_logit(const void* p, int64_t i) { return to_float(static_cast<const T*>(p)[i]); }
 template <>
@@ -223,7 +185,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteParams p) {
       else u = (uint32_t)fminf(fmaxf((16.f - (top - l[v])) * 0x1p18f, 1.f), (float)kMostKey);
       key[v] = l[v] > -kInf ? u << 10 | (1023 - (v * LANES + lane)) : 0u;
     }
-    if constexpr (!kWhole) close = top == kInf;  // no distances
+    if constexpr (!kWhole) close = __ballot(top == kInf) != 0;  // no distances: all keys are the lowest
   }
   int mine, slot = lane;
   const bool listed = choose_packed<LANES, V>(key, p.topk, kWhole ? 0u : BIAS ? 9u : 1u, mine, close);

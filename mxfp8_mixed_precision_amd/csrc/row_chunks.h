@@ -1,5 +1,5 @@
-// Rows of a tensor in chunks of 8 elements, as the kernels that stream rows (norms, experts' rows) move them; sums across
-// the lanes of a row; the MXFP8 codes of a chunk.
+// Rows of a tensor in chunks of 8 elements, as the kernels that stream rows (norms, experts' rows) move them; sums and
+// other operations across the lanes of a row; the MXFP8 codes of a chunk.
 #pragma once
 
 #include <type_traits>
@@ -198,6 +198,44 @@ __device__ __forceinline__ float lanes_sum(float v) {
   if constexpr (LANES == 64) {
     const int lane = threadIdx.x & 63;
     v += __int_as_float(__builtin_amdgcn_ds_bpermute((lane ^ 32) << 2, __float_as_int(v)));  // lane ^ 32
+  }
+  return v;
+}
+
+// op over the values of the lane's LANES (16, 32 or 64) lanes, in every lane.
+template <int LANES, class V, class Op>
+__device__ __forceinline__ V lanes_all(V v, Op op) {
+  constexpr int kWords = sizeof(V) / 4;
+  struct Words {
+    int w[kWords];
+  };
+  const auto ror = [](V x, auto n) {  // row_ror within 16 lanes
+    Words u = __builtin_bit_cast(Words, x);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) u.w[i] = __builtin_amdgcn_mov_dpp(u.w[i], 0x120 + decltype(n)::value, 0xF, 0xF, false);
+    return __builtin_bit_cast(V, u);
+  };
+  v = op(v, ror(v, std::integral_constant<int, 8>{}));
+  v = op(v, ror(v, std::integral_constant<int, 4>{}));
+  v = op(v, ror(v, std::integral_constant<int, 2>{}));
+  v = op(v, ror(v, std::integral_constant<int, 1>{}));
+  if constexpr (LANES >= 32) {  // the two rows of 16 of each half
+    Words a = __builtin_bit_cast(Words, v), b;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const u32x2 both = __builtin_amdgcn_permlane16_swap((unsigned)a.w[i], (unsigned)a.w[i], false, false);
+      a.w[i] = (int)both[0], b.w[i] = (int)both[1];
+    }
+    v = op(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b));
+  }
+  if constexpr (LANES == 64) {
+    Words a = __builtin_bit_cast(Words, v), b;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const u32x2 both = __builtin_amdgcn_permlane32_swap((unsigned)a.w[i], (unsigned)a.w[i], false, false);
+      a.w[i] = (int)both[0], b.w[i] = (int)both[1];
+    }
+    v = op(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b));
   }
   return v;
 }

@@ -128,11 +128,10 @@ __device__ __forceinline__ float silu(float x) {
   return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.4426950408889634f));
 }
 
-// Sum over the wave's lanes.
-__device__ __forceinline__ int64_t wave_sum(int64_t v) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
-  return v;
+// Sum over the wave's lanes of values from 0 to 2^31 - 1: its halves' sums in 32 bits.
+__device__ __forceinline__ int64_t wave_sum(int v) {
+  const auto add = [](int a, int b) { return a + b; };
+  return ((int64_t)lanes_all<64>(v >> 16, add) << 16) + lanes_all<64>(v & 0xFFFF, add);
 }
 
 // Every wave's LDS accesses so far have ended, and the barrier: copies and loads stay on their way.
@@ -151,7 +150,7 @@ struct W4Job {
     first1 = gated ? n0 : min(n0 + 16, N - 1);
     if (p.m_splits != nullptr) {  // this expert's rows and weights
       const int g = blockIdx.y, lane = threadIdx.x & 63;
-      for (int e0 = 0; e0 < g; e0 += 64) t0 += wave_sum(e0 + lane < g ? (int64_t)max(p.m_splits[e0 + lane], 0) : 0);
+      for (int e0 = 0; e0 < g; e0 += 64) t0 += wave_sum(e0 + lane < g ? max(p.m_splits[e0 + lane], 0) : 0);
       t_end = min(t0 + max(p.m_splits[g], 0), p.M);
       w_row = (int64_t)g * (gated ? 2 * N : N);
     } else {
