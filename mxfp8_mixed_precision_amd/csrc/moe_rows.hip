@@ -139,21 +139,22 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(RowsParams p, int chu
   store_chunk(static_cast<T*>(p.y) + token * p.cols + c, pack<T>(sum), p.cols - c);
 }
 
-// A wave takes one slot: w dy to its row and the dot product of dy with the experts' output there.
-template <class T, bool STREAM>
+// LANES lanes take one slot: w dy to its row and the dot product of dy with the experts' output there.  (More chunks of a
+// lane in flight made it slower: 65536 rows of 4096 bf16 216 us, with 4 chunks ahead 225.)
+template <class T, bool STREAM, int LANES>
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(RowsParams p) {
-  const int lane = threadIdx.x & 63;
-  const int64_t slot = (p.block0 + blockIdx.x) * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (slot >= p.tokens * p.topk) return;
-  const int64_t token = slot / p.topk;
-  const int row = p.row_of[slot];
-  const int64_t r = row < p.total_rows ? row : -1;
+  const int lane = threadIdx.x % LANES;
+  int64_t slot = (p.block0 + blockIdx.x) * (kThreads / LANES);
+  slot += LANES == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / LANES) : threadIdx.x / LANES;
+  const bool ok = slot < p.tokens * p.topk;
+  const int row = ok ? p.row_of[slot] : -1;
+  const bool there = row >= 0 && row < p.total_rows;
   float dot = 0.f;
-  if (r >= 0) {
+  if (there) {
     const float w = p.weights[slot];
-    const T* dy = static_cast<const T*>(p.x) + token * p.cols;
-    const T* out = static_cast<const T*>(p.rows) + r * p.cols;
-        for (int c0 = 0; c0 < p.cols; c0 += 64 * kChunk) {  // every lane takes part in the quads' exchanges
+    const T* dy = static_cast<const T*>(p.x) + slot / p.topk * p.cols;
+    const T* out = static_cast<const T*>(p.rows) + (int64_t)row * p.cols;
+    for (int c0 = 0; c0 < p.cols; c0 += LANES * kChunk) {  // every lane takes part in the quads' exchanges
       const int c = c0 + lane * kChunk;
       float g[kChunk], f[kChunk];
       load_floats(dy, c, p.cols, g);
@@ -166,15 +167,15 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(RowsParams p
         g[e] *= w;
       }
       const Raw<T> v = pack<T>(g);
-      const int64_t at = r * p.cols + c;
+      const int64_t at = (int64_t)row * p.cols + c;
       if (p.y != nullptr) put_chunk<T, STREAM>(static_cast<T*>(p.y) + at, v, p.cols - c);
       if constexpr (std::is_same_v<T, bf16_t>) {
         if (p.q != nullptr) store_mx(v, p.q, p.q_scale, at, c < p.cols, p.q_e5m2);
       }
     }
   }
-  dot = lanes_sum<64>(dot);
-  if (lane == 0) p.dweights[slot] = dot;
+  dot = lanes_sum<LANES>(dot);
+  if (ok && lane == 0) p.dweights[slot] = dot;
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -219,13 +220,18 @@ te_status run_combine(const RowsParams& p, hipStream_t stream) {
   });
 }
 
+template <class T, int LANES>
+te_status run_combine_backward(const RowsParams& p, hipStream_t stream) {
+  const int64_t per = kThreads / LANES;
+  return in_parts(p, (p.tokens * p.topk + per - 1) / per, [&](const RowsParams& q, dim3 grid) {
+    if (streams<T>(q)) hipLaunchKernelGGL((combine_backward_kernel<T, true, LANES>), grid, dim3(kThreads), 0, stream, q);
+    else hipLaunchKernelGGL((combine_backward_kernel<T, false, LANES>), grid, dim3(kThreads), 0, stream, q);
+  });
+}
+
 template <class T>
 te_status run_combine_backward(const RowsParams& p, hipStream_t stream) {
-  const int64_t per = kThreads / 64;
-  return in_parts(p, (p.tokens * p.topk + per - 1) / per, [&](const RowsParams& q, dim3 grid) {
-    if (streams<T>(q)) hipLaunchKernelGGL((combine_backward_kernel<T, true>), grid, dim3(kThreads), 0, stream, q);
-    else hipLaunchKernelGGL((combine_backward_kernel<T, false>), grid, dim3(kThreads), 0, stream, q);
-  });
+  return p.cols <= 256 ? run_combine_backward<T, 16>(p, stream) : run_combine_backward<T, 64>(p, stream);
 }
 
 te_status check_rows(te_dtype dtype, int64_t tokens, int64_t cols, int topk, int64_t total_rows, const uint8_t* q,
