@@ -212,7 +212,8 @@ __device__ __forceinline__ V lanes_all(V v, Op op) {
   const auto ror = [](V x, auto n) {  // row_ror within 16 lanes
     Words u = __builtin_bit_cast(Words, x);
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) u.w[i] = __builtin_amdgcn_mov_dpp(u.w[i], 0x120 + decltype(n)::value, 0xF, 0xF, false);
+    for (int i = 0; i < kWords; ++i)
+      u.w[i] = __builtin_amdgcn_mov_dpp(u.w[i], 0x120 + decltype(n)::value, 0xF, 0xF, false);
     return __builtin_bit_cast(V, u);
   };
   v = op(v, ror(v, std::integral_constant<int, 8>{}));

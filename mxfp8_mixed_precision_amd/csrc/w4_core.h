@@ -4,13 +4,23 @@
 //   D = P, or act(P[:, :N]) * P[:, N:]
 // q are the codes of INT4 (0 .. 15, z the zero point, 8 without one) or E2M1 (z = 0).
 //
-// A workgroup takes 16 NF rows of W (output columns, or 16 columns' gate and up rows); its waves deal the K steps of 128
-// among themselves and their partial sums meet in LDS, in wave order.  Lane 16 q + r loads 16 bytes of row r, the codes
-// of the step's 32-block q; a 4 x 4 transpose across the lanes gives MFMA i (16 x 16 x 32) block i: lane 16 q + r holds
-// codes 8 q .. 8 q + 7 of row r, turned into bf16 / fp16 by exact conversions (a code 0 .. 15 is the E4M3 code of
-// 2^-9 times itself).  The weights are the MFMA's second operand, so that a lane's results are of one weight row, whose
-// scale the lane holds.  Products and sums are fp32; a group's sum is scaled in fp32, after its zero point times the sum
-// of x, which another MFMA gives with ones for weights.
+// A workgroup takes 16 NF rows of W (output columns, or 16 columns' gate and up rows); its waves deal the K steps of
+// 128 among themselves and their partial sums meet in LDS, in wave order (deterministic).  Lane 16 q + r loads 16
+// bytes of row r, the codes of the step's 32-block q; a 4 x 4 transpose across the lanes gives MFMA i (16 x 16 x 32)
+// block i: lane 16 q + r holds codes 8 q .. 8 q + 7 of row r, turned into bf16 / fp16 by exact conversions (a code 0
+// .. 15 is the E4M3 code of 2^-9 times itself).  The weights are the MFMA's second operand, so that a lane's results
+// are of one weight row, whose scale the lane holds.  Products and sums are fp32; a group's sum is scaled in fp32,
+// after its zero point times the sum of x, which another MFMA gives with ones for weights.
+//
+// The weights' bytes bound one to four rows (w4_few_kernel), with 149 vector instructions for the 2 KB of a step that
+// take half of the time themselves; with more rows (w4_ring_kernel) every workgroup's reading of all of x does, the more
+// the more rows: a CU takes in ~75 bytes a ns from L2, 917 KB of 32 x 14336 in 12 us.  Loading x and the scales where
+// they are used, straight into the MFMA's layout, took 1.5 to 2 times as long: such a load takes 64 bytes of each of 16
+// rows, and loads return in order, so that each waits for the weights' ones before it.
+// Measured on MI355X, us a kernel, inputs of three calls in turn: one row, N = 14336 gated, K = 4096, groups of 128:
+// 15.6 (61 MB, 3.9 TB/s; with its caller's other calls around it 14.0, 4.3 TB/s; a large copy 5.0); 64 rows over 32
+// experts, N = 1536, K = 4096: 27 (91 MB); 32 rows, N = 4096, K = 14336, E2M1 in groups of 32: 18.3 (39 MB of weights
+// and x); 5 rows, N = 1001, K = 2080: 6.2, latencies.
 #pragma once
 
 #include "gemm_core.h"
@@ -60,7 +70,9 @@ constexpr int kBeyond = 0x60000000;     // an offset past the end of every buffe
 template <class T> struct Half;  // the activations' type in the MFMA
 template <> struct Half<bf16_t> {
   typedef v8bf v8;
-  static __device__ __forceinline__ v4f mfma(v8 a, v8 b, v4f c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+  static __device__ __forceinline__ v4f mfma(v8 a, v8 b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
   template <bool HI>
   static __device__ __forceinline__ uint32_t from_e4m3(uint32_t v) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 512.f, HI));
@@ -73,7 +85,9 @@ template <> struct Half<bf16_t> {
 };
 template <> struct Half<f16_t> {
   typedef v8h v8;
-  static __device__ __forceinline__ v4f mfma(v8 a, v8 b, v4f c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+  static __device__ __forceinline__ v4f mfma(v8 a, v8 b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
   template <bool HI>
   static __device__ __forceinline__ uint32_t from_e4m3(uint32_t v) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v, 512.f, HI));
@@ -181,7 +195,8 @@ __device__ __forceinline__ Unaligned<V, COUNT> load_unaligned(const void* p) {
 
 // The scales and zero points of groups g0 .. g1 - 1 of the workgroup's weight rows to LDS, [group][weight row].
 template <class T, bool ZERO, int THREADS, int ROWS>
-__device__ __forceinline__ void fill_tables(const W4Params& p, const W4Job& job, int g0, int g1, float* scales, uint8_t* zeros) {
+__device__ __forceinline__ void fill_tables(const W4Params& p, const W4Job& job, int g0, int g1, float* scales,
+                                            uint8_t* zeros) {
   constexpr int kShare = THREADS / ROWS, kAtOnce = 8;  // threads of a row; groups of a thread
   const int row = threadIdx.x / kShare;
   const int64_t from = job.weight_row(row >> 4, row & 15) * p.per_row;
@@ -220,8 +235,8 @@ __device__ __forceinline__ void fill_tables(const W4Params& p, const W4Job& job,
   }
 }
 
-// A wave's sums: of NF fragments of 16 weight rows and MF fragments of 16 rows of x.  Lane (q, r), element e: row 4 q + e
-// of x, weight row r.
+// A wave's sums: of NF fragments of 16 weight rows and MF fragments of 16 rows of x.  Lane (q, r), element e: row 4 q
+// + e of x, weight row r.
 template <class T, te_w4_format FMT, int NF, int MF>
 struct W4Sums {
   static constexpr bool kInt = FMT == TE_W4_INT4;
@@ -249,7 +264,8 @@ struct W4Sums {
 #pragma unroll
     for (int j = 0; j < MF; ++j)
       if constexpr (kInt)
-        xsum[j] = Half<T>::mfma(__builtin_bit_cast(v8, x[j]), __builtin_bit_cast(v8, u32x4{one, one, one, one}), xsum[j]);
+        xsum[j] = Half<T>::mfma(__builtin_bit_cast(v8, x[j]), __builtin_bit_cast(v8, u32x4{one, one, one, one}),
+                                xsum[j]);
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
       const v8 wf = weights<T, FMT>(codes[f]);
@@ -273,11 +289,11 @@ struct W4Sums {
         }
     }
   }
-  // A step (4 blocks from `block` on): its codes, transposed, and x in LDS, in rows of 256 bytes whose piece c of 16 bytes
-  // lies at place c ^ (row % 16).
+  // A step (4 blocks from `block` on): its codes, transposed, and x in LDS, in rows of 256 bytes whose piece c of 16
+  // bytes lies at place c ^ (row % 16).
   template <int RX, W4Groups GROUPS>
-  __device__ __forceinline__ void step(const W4Params& p, const u32x4 (&codes)[NF], const uint8_t* x_at, int block, int g0,
-                                       const float* scales, const uint8_t* zeros) {
+  __device__ __forceinline__ void step(const W4Params& p, const u32x4 (&codes)[NF], const uint8_t* x_at, int block,
+                                       int g0, const float* scales, const uint8_t* zeros) {
     const int q = (threadIdx.x & 63) >> 4, r = threadIdx.x & 15;
     u32x4 x[4][MF];
 #pragma unroll
@@ -357,15 +373,17 @@ struct W4Sums {
   }
 };
 
-// Up to RX = 4 rows at a time: the weights bound them.  x and the scales of a chunk of K lie in LDS, copied by all waves;
-// the codes of U steps of a wave are on their way in registers.
+// Up to RX = 4 rows at a time: the weights bound them.  x and the scales of a chunk of K lie in LDS, copied by all
+// waves; the codes of U steps of a wave are on their way in registers.
 template <int W_, int NF_, int RX_, int U_, int CHUNK_ = 32>
 struct W4Few {
   static constexpr int W = W_, NF = NF_, RX = RX_, U = U_, kRows = 16 * NF, MF = 1;
   static constexpr bool kFew = true;
   static constexpr int kChunk = CHUNK_;  // steps
   static constexpr int kX = kChunk * RX * 256, kPart = W * NF * 1024, kArena = kX > kPart ? kX : kPart;
-  static constexpr int kGroups(W4Groups groups) { return groups == W4Groups::Steps ? kChunk + 1 : 4 * kChunk + 4; }  // with the tail's
+  static constexpr int kGroups(W4Groups groups) {  // of a chunk, and the tail's
+    return groups == W4Groups::Steps ? kChunk + 1 : 4 * kChunk + 4;
+  }
   static_assert(kChunk % (W * U) == 0 && U % 2 == 0 && kChunk * RX % (4 * W) == 0);
 };
 
@@ -399,7 +417,8 @@ __global__ __launch_bounds__(64 * C::W) void w4_few_kernel(W4Params p) {
       const int step = step_of(n);
 #pragma unroll
       for (int f = 0; f < NF; ++f)
-        codes[u][f] = __builtin_amdgcn_raw_buffer_load_b128(rw[f], vw[f], step < steps ? step * (kStep / 2) : kBeyond, 0);
+        codes[u][f] =
+            __builtin_amdgcn_raw_buffer_load_b128(rw[f], vw[f], step < steps ? step * (kStep / 2) : kBeyond, 0);
       __builtin_amdgcn_sched_barrier(0);
     };
     const i32x4 rx = make_rsrc(static_cast<const T*>(p.x) + t0 * p.K, rows * p.K * 2);
@@ -409,8 +428,8 @@ __global__ __launch_bounds__(64 * C::W) void w4_few_kernel(W4Params p) {
 #pragma unroll
       for (int i = 0; i < C::kChunk / kPer / W; ++i) {
         const int at = wave + W * i, step = s0 + at * kPer, m = RX == 1 ? 0 : q, s = RX == 1 ? q : 0;
-        lds_dma16(rx, x_lds + at * 1024, m < rows && step + s < steps ? (int)(m * p.K * 2) + s * 256 + 16 * (r ^ m) : kBeyond,
-                  step < steps ? step * (kStep * 2) : kBeyond);
+        const int from = m < rows && step + s < steps ? (int)(m * p.K * 2) + s * 256 + 16 * (r ^ m) : kBeyond;
+        lds_dma16(rx, x_lds + at * 1024, from, step < steps ? step * (kStep * 2) : kBeyond);
       }
     };
 
@@ -427,7 +446,8 @@ __global__ __launch_bounds__(64 * C::W) void w4_few_kernel(W4Params p) {
         lds_barrier();
         copy(s0);
       }
-      fill_tables<T, kInt, 64 * W, C::kRows>(p, job, g0, s1 == steps ? p.per_row : w4_group(p, 4 * s1 - 1) + 1, scales, zeros);
+      const int g1 = s1 == steps ? p.per_row : w4_group(p, 4 * s1 - 1) + 1;
+      fill_tables<T, kInt, 64 * W, C::kRows>(p, job, g0, g1, scales, zeros);
       wait_vmcnt<0>();
       lds_barrier();
 #pragma unroll 1
@@ -439,7 +459,8 @@ __global__ __launch_bounds__(64 * C::W) void w4_few_kernel(W4Params p) {
 #pragma unroll
           for (int f = 0; f < NF; ++f) now[f] = transpose_blocks(codes[u][f]);
           load(u, n + U);
-          if (step < s1) sums.template step<RX, GROUPS>(p, now, arena + (step - s0) * (RX * 256), 4 * step, g0, scales, zeros);
+          if (step < s1)
+            sums.template step<RX, GROUPS>(p, now, arena + (step - s0) * (RX * 256), 4 * step, g0, scales, zeros);
         }
       }
     }
@@ -449,8 +470,8 @@ __global__ __launch_bounds__(64 * C::W) void w4_few_kernel(W4Params p) {
   }
 }
 
-// Tiles of RX = 16 or 32 rows: what a workgroup reads of x bounds them.  Each wave keeps D steps, x and codes, in LDS of
-// its own, D - 1 of them on their way, and waits for nobody.
+// Tiles of RX = 16 or 32 rows: what a workgroup reads of x bounds them.  Each wave keeps D steps, x and codes, in LDS
+// of its own, D - 1 of them on their way, and waits for nobody.
 template <int W_, int NF_, int RX_, int D_>
 struct W4Ring {
   static constexpr int W = W_, NF = NF_, RX = RX_, D = D_, kRows = 16 * NF, MF = RX / 16;
@@ -496,7 +517,8 @@ __global__ __launch_bounds__(64 * C::W) void w4_ring_kernel(W4Params p) {
     const auto issue = [&](int slot, int step, bool there) {
       const uint32_t to = ring + slot * C::kSlot;
 #pragma unroll
-      for (int f = 0; f < NF; ++f) lds_dma16(rw[f], to + RX * 256 + f * 1024, vw[f], there ? step * (kStep / 2) : kBeyond);
+      for (int f = 0; f < NF; ++f)
+        lds_dma16(rw[f], to + RX * 256 + f * 1024, vw[f], there ? step * (kStep / 2) : kBeyond);
 #pragma unroll
       for (int j = 0; j < RX / 4; ++j) lds_dma16(rx, to + j * 1024, vx[j], there ? step * (kStep * 2) : kBeyond);
     };
@@ -512,7 +534,8 @@ __global__ __launch_bounds__(64 * C::W) void w4_ring_kernel(W4Params p) {
       for (int n = 0; n < D - 1; ++n) issue(n, step_of(n), step_of(n) < s1);
       g0 = w4_group(p, 4 * s0);
       if (s0 > 0) lds_barrier();
-      fill_tables<T, kInt, 64 * W, C::kRows>(p, job, g0, s1 == steps ? p.per_row : w4_group(p, 4 * s1 - 1) + 1, scales, zeros);
+      const int g1 = s1 == steps ? p.per_row : w4_group(p, 4 * s1 - 1) + 1;
+      fill_tables<T, kInt, 64 * W, C::kRows>(p, job, g0, g1, scales, zeros);
       lds_barrier();
       for (int n = 0; step_of(n) < s1; ++n) {
         wait_vmcnt<(D - 2) * C::kCopies>();  // this step's copies; the reads of the slot filled next have ended
@@ -561,18 +584,38 @@ te_status w4_by_group(const W4Params& p, hipStream_t stream) {
   return launch_w4<T, FMT, C, W4Groups::Any>(p, stream);
 }
 
+// Kernels by the rows of a tile and by the tiles of 16 NF weight rows.  Many tiles (3 a CU): small workgroups,
+// several on a CU, whose starts and ends overlap; few: as many waves as there are on one tile.  us with the one and
+// the other:
+//   1 row:  N = 14336 gated, K = 4096 (896 tiles) 2 waves 15.8, 8 waves 23.7;  N = 4096, K = 14336 (256) 22.5 and 12.6
+//   3 rows: N = 28672, K = 4096 4 waves 18.3, 8 waves 29.4;  N = 4096, K = 14336 15.4 and 13.9;  N = 8192, K = 4096 (512)
+//           8.6 and 9.3, so that 8 waves need a long K;  N = 28672, K = 1024 2 waves 9.3, 4 waves 12.2: a short K
+//   16 rows: N = 14336 gated, K = 4096 4 waves and 2 slots 21.4, 8 and 3 32.1;  N = K = 4096 (256) 8.2 and 7.9
+//   32 rows: the same N 3 waves 32.0, 7 waves 38.0;  N = 4096, K = 14336 27.9 and 19.5;  64 rows of N = K = 4096 (512 tiles
+//           with their two tiles of rows) 13.6 and 17.0
+// Two fragments a wave where many tiles are left of them (64 rows over 32 experts, N = 1536: 28.0, one fragment
+// 28.4).
 template <class T, te_w4_format FMT, int NF>
 te_status w4_by_rows(const W4Params& p, int64_t rows, int64_t tiles, hipStream_t stream) {
   const int64_t cus = device_cu_count();
-  const bool many = tiles >= 3 * cus, ring_many = 2 * tiles * (p.m_splits != nullptr ? 1 : (p.M + 31) / 32) > 3 * cus;
-  if (rows <= 1) return many ? w4_by_group<T, FMT, W4Few<2, NF, 1, 2>>(p, stream) : w4_by_group<T, FMT, W4Few<8, NF, 1, 2>>(p, stream);
+  const bool many = tiles >= 3 * cus;
+  // a workgroup of the ring kernels has a CU's LDS for itself, or shares it: with tiles of rows beside each other
+  const bool ring_many = 2 * tiles * (p.m_splits != nullptr ? 1 : (p.M + 31) / 32) > 3 * cus;
+  if (rows <= 1) {
+    if (many) return w4_by_group<T, FMT, W4Few<2, NF, 1, 2>>(p, stream);
+    return w4_by_group<T, FMT, W4Few<8, NF, 1, 2>>(p, stream);
+  }
   if (rows <= 4) {
     if (many && p.K <= 2048) return w4_by_group<T, FMT, W4Few<2, NF, 4, 2, 16>>(p, stream);
     if (!many && p.K >= 8192) return w4_by_group<T, FMT, W4Few<8, NF, 4, 2>>(p, stream);
     return w4_by_group<T, FMT, W4Few<4, NF, 4, 2>>(p, stream);
   }
-  if (rows <= 16) return ring_many ? w4_by_group<T, FMT, W4Ring<4, NF, 16, 2>>(p, stream) : w4_by_group<T, FMT, W4Ring<8, NF, 16, 3>>(p, stream);
-  return ring_many ? w4_by_group<T, FMT, W4Ring<3, NF, 32, 2>>(p, stream) : w4_by_group<T, FMT, W4Ring<7, NF, 32, 2>>(p, stream);
+  if (rows <= 16) {
+    if (ring_many) return w4_by_group<T, FMT, W4Ring<4, NF, 16, 2>>(p, stream);
+    return w4_by_group<T, FMT, W4Ring<8, NF, 16, 3>>(p, stream);
+  }
+  if (ring_many) return w4_by_group<T, FMT, W4Ring<3, NF, 32, 2>>(p, stream);
+  return w4_by_group<T, FMT, W4Ring<7, NF, 32, 2>>(p, stream);
 }
 
 template <class T, te_w4_format FMT>

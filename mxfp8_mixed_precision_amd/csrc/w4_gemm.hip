@@ -28,7 +28,8 @@ te_status run(const W4Params& p, te_dtype dtype, te_w4_format fmt, te_dtype d_dt
   return fmt == TE_W4_INT4 ? launch_w4_fp16_int4(p, stream) : launch_w4_fp16_e2m1(p, stream);
 }
 
-te_status run_grouped(const W4Params& p, te_dtype dtype, te_w4_format fmt, te_dtype d_dtype, bool gated, hipStream_t stream) {
+te_status run_grouped(const W4Params& p, te_dtype dtype, te_w4_format fmt, te_dtype d_dtype, bool gated,
+                      hipStream_t stream) {
   TE_REQUIRE(p.groups >= 1 && p.groups <= kW4MaxGroups, TE_ERR_SHAPE);
   TE_REQUIRE(p.N > 0 && p.K > 0, TE_ERR_SHAPE);
   TE_REQUIRE(p.m_splits != nullptr, TE_ERR_NULL);
