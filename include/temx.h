@@ -587,7 +587,7 @@ te_status te_mxfp8_grouped_dgated_gemm(int32_t num_groups, const int32_t* m_spli
  *   normalize 0 or 1;  scale finite
  *   experts  int32 [tokens, topk], weights float [tokens, topk]
  *   num_experts 1 .. 1024, topk 1 .. min(num_experts, 64), tokens >= 0,
- *   tokens * topk < 2^31 - 65536.
+ *   tokens * topk < 2^31 - 65536.  No output may overlap an input.
  * An expert whose logit (or logit's sum with the bias) is NaN is not chosen; a
  * NaN logit makes the softmax shares (normalize = 0) of its token NaN.
  */
@@ -622,6 +622,7 @@ te_status te_moe_route_backward(te_score score, const void* logits, te_dtype dty
  *   workspace device scratch of at least te_moe_sort_workspace_size(slots,
  *             num_experts) bytes, 4-byte aligned (NULL where that is 0).  Calls
  *             that may run at the same time need workspaces of their own.
+ *   No output and no workspace may overlap an input or another output.
  * slots == 0 writes zeros to m_splits.
  */
 size_t te_moe_sort_workspace_size(int64_t slots, int32_t num_experts);
@@ -667,7 +668,8 @@ te_status te_moe_combine(const void* rows, te_dtype dtype, int64_t total_rows, i
  *   dy       dtype [tokens, cols]; rows dtype [total_rows, cols]: what the
  *            forward combined
  *   drows    dtype [total_rows, cols], NULL where q is given; rows of no slot
- *            stay as they were.  drows may be rows itself.
+ *            stay as they were.  drows may be rows itself; nothing else may
+ *            overlap.
  *   q, q_scale both or neither: drows as MXFP8 operand, as te_moe_dispatch's
  *   dweights float [tokens, topk]
  *   The rest as te_moe_dispatch.
@@ -697,7 +699,8 @@ te_status te_moe_combine_backward(const void* dy, const void* rows, te_dtype dty
  *   Shapes: any M, N >= 0 (any M is right; from about 64 rows up a GEMM on
  *   quantized activations is the faster one); M, 2N < 2^31 - 65536, K <= 2^23.
  *   M == 0 or N == 0 enqueues nothing; K == 0 gives P = bias.
- *   x, w and d are 16-byte aligned; scales and bias to their type.
+ *   x, w and d are 16-byte aligned; scales and bias to their type.  d may not
+ *   overlap an input.
  *   A non-finite value of x affects its own row of D only; with TE_W4_INT4 an
  *   infinite one gives NaN where the formula gives an infinity.
  */
