@@ -14,6 +14,7 @@
 // (6.6 us of vector instructions, then the waves that compare near sums exactly), 8.7 to 10.4 without, where the
 // logits alone take 3.3 (fp32).  With 64-bit keys for all and a maximum and a minimum a slot the same took 20 us.
 // The backward reads and writes the logits' tensor at 2.8 TB/s (16384 x 256 fp32 softmax shares: 12.5 us).
+#include <algorithm>
 #include <type_traits>
 
 #include "row_chunks.h"
@@ -33,7 +34,7 @@ struct RouteParams {
   float* weights;          // forward
   const float* dweights;   // backward
   void* dlogits;           // backward
-  int64_t tokens;
+  int64_t token0, tokens;  // a launch's first token, the one behind its last
   int num_experts, topk;
   float scale;
   bool sigmoid, normalize;
@@ -136,7 +137,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteParams p) {
   constexpr bool kWhole = !BIAS && sizeof(T) == 2;
   constexpr uint32_t kMostKey = (1u << 22) - 1;
   const int lane = threadIdx.x % LANES;
-  const int64_t token = (int64_t)blockIdx.x * (kRouteThreads / LANES) + threadIdx.x / LANES;
+  const int64_t token = p.token0 + (int64_t)blockIdx.x * (kRouteThreads / LANES) + threadIdx.x / LANES;
   const bool ok = token < p.tokens;  // every lane takes part in the exchanges
   const int64_t at = (ok ? token : 0) * p.num_experts;
   const auto sum = [](auto a, auto b) { return a + b; };
@@ -248,7 +249,7 @@ template <class T, int LANES, int V>
 __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteParams p) {
   __shared__ float slots[kRouteThreads / LANES][V * LANES];
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
-  const int64_t token = (int64_t)blockIdx.x * (kRouteThreads / LANES) + group;
+  const int64_t token = p.token0 + (int64_t)blockIdx.x * (kRouteThreads / LANES) + group;
   const bool ok = token < p.tokens;
   const int64_t at = (ok ? token : 0) * p.num_experts;
   const auto sum = [](float a, float b) { return a + b; };
@@ -490,14 +491,22 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortParams p) 
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+constexpr int64_t kMostTokens = (int64_t)1 << 25;  // of one launch: 2^31 threads and fewer
+
 template <class T, int LANES, int V>
-te_status launch_route(const RouteParams& p, bool backward, hipStream_t stream) {
+te_status launch_route(RouteParams p, bool backward, hipStream_t stream) {
   constexpr int kPer = kRouteThreads / LANES;
-  const dim3 grid((unsigned)((p.tokens + kPer - 1) / kPer)), block(kRouteThreads);
-  if (backward) hipLaunchKernelGGL((route_backward_kernel<T, LANES, V>), grid, block, 0, stream, p);
-  else if (p.bias != nullptr) hipLaunchKernelGGL((route_kernel<T, LANES, V, true>), grid, block, 0, stream, p);
-  else hipLaunchKernelGGL((route_kernel<T, LANES, V, false>), grid, block, 0, stream, p);
-  return launch_status();
+  const int64_t tokens = p.tokens;
+  for (p.token0 = 0; p.token0 < tokens; p.token0 += kMostTokens) {
+    p.tokens = std::min(tokens, p.token0 + kMostTokens);
+    const dim3 grid((unsigned)((p.tokens - p.token0 + kPer - 1) / kPer)), block(kRouteThreads);
+    if (backward) hipLaunchKernelGGL((route_backward_kernel<T, LANES, V>), grid, block, 0, stream, p);
+    else if (p.bias != nullptr) hipLaunchKernelGGL((route_kernel<T, LANES, V, true>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((route_kernel<T, LANES, V, false>), grid, block, 0, stream, p);
+    const te_status st = launch_status();
+    if (st != TE_OK) return st;
+  }
+  return TE_OK;
 }
 
 template <class T>
@@ -546,7 +555,7 @@ extern "C" te_status te_moe_route(te_score score, const void* logits, te_dtype d
   TE_REQUIRE(logits && experts && weights, TE_ERR_NULL);
   TE_REQUIRE(aligned16(logits) && aligned4(bias) && aligned4(experts) && aligned4(weights), TE_ERR_ALIGN);
   TE_REQUIRE(device_is_gfx950(), TE_ERR_ARCH);
-  const RouteParams p{logits, bias, experts, weights, nullptr, nullptr, tokens, num_experts, topk, scale,
+  const RouteParams p{logits, bias, experts, weights, nullptr, nullptr, 0, tokens, num_experts, topk, scale,
                       score == TE_SCORE_SIGMOID, normalize != 0};
   return run_route(p, dtype, false, stream);
 }
@@ -561,8 +570,8 @@ extern "C" te_status te_moe_route_backward(te_score score, const void* logits, t
   TE_REQUIRE(logits && experts && dweights && dlogits, TE_ERR_NULL);
   TE_REQUIRE(aligned16(logits) && aligned16(dlogits) && aligned4(experts) && aligned4(dweights), TE_ERR_ALIGN);
   TE_REQUIRE(device_is_gfx950(), TE_ERR_ARCH);
-  const RouteParams p{logits, nullptr, const_cast<int32_t*>(experts), nullptr, dweights, dlogits, tokens, num_experts,
-                      topk, scale, score == TE_SCORE_SIGMOID, normalize != 0};
+  const RouteParams p{logits, nullptr, const_cast<int32_t*>(experts), nullptr, dweights, dlogits, 0, tokens,
+                      num_experts, topk, scale, score == TE_SCORE_SIGMOID, normalize != 0};
   return run_route(p, dtype, true, stream);
 }
 

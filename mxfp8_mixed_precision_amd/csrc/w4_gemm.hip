@@ -13,8 +13,9 @@ te_status run(const W4Params& p, te_dtype dtype, te_w4_format fmt, te_dtype d_dt
   TE_REQUIRE(p.scale_dtype == dtype || p.scale_dtype == TE_FP32 || p.scale_dtype == TE_E8M0, TE_ERR_DTYPE);
   TE_REQUIRE(d_dtype == dtype || d_dtype == TE_FP32, TE_ERR_DTYPE);
   constexpr int64_t kMostSize = ((int64_t)1 << 31) - 65536;
-  // K: the kernels' offsets into 64 rows of x and 16 of W are of 32 bits
-  TE_REQUIRE(p.M >= 0 && p.M <= kMostSize && p.N >= 0 && p.N <= kMostSize / 2, TE_ERR_SHAPE);
+  // N: a launch has fewer than 2^32 threads side by side; K: the kernels' offsets into 64 rows of x and 16 of W are of
+  // 32 bits
+  TE_REQUIRE(p.M >= 0 && p.M <= kMostSize && p.N >= 0 && p.N <= (int64_t)1 << 26, TE_ERR_SHAPE);
   TE_REQUIRE(p.K >= 0 && p.K <= (int64_t)1 << 23, TE_ERR_SHAPE);
   TE_REQUIRE(p.group >= 32 && p.group % 32 == 0 && p.K % p.group == 0, TE_ERR_SHAPE);
   TE_REQUIRE(p.groups >= 1 && p.groups <= kW4MaxGroups, TE_ERR_SHAPE);

@@ -127,6 +127,23 @@ def test_route_masked_infinite_and_nan():
     np.testing.assert_allclose(f64(w)[0], [0.25] * 4 + [0.0] * 5, rtol=1e-6)
 
 
+def test_route_of_more_tokens_than_a_launch_takes():
+    """Two launches: tokens on both sides of the border and the last ones, against the same tokens alone."""
+    tokens = (1 << 25) + 1001
+    g = torch.Generator(device="cuda")
+    g.manual_seed(302)
+    x = torch.randn((tokens, 4), generator=g, device="cuda", dtype=torch.float32).half()
+    dw = torch.randn((tokens, 2), generator=g, device="cuda")
+    e, w = te().moe_route("softmax", x, 2, normalize=False)
+    dx = te().moe_route_backward("softmax", x, e, dw, normalize=False)
+    for a in (0, (1 << 25) - 500, tokens - 64):
+        part = x[a:a + 600].clone()
+        pe, pw = te().moe_route("softmax", part, 2, normalize=False)
+        pdx = te().moe_route_backward("softmax", part, pe, dw[a:a + 600].clone(), normalize=False)
+        assert torch.equal(e[a:a + 600], pe) and torch.equal(w[a:a + 600], pw) and torch.equal(dx[a:a + 600], pdx)
+    assert torch.equal(torch.gather(x, 1, e.long()), x.sort(dim=1, descending=True).values[:, :2])
+
+
 def test_route_no_tokens():
     got, w = te().moe_route("softmax", torch.zeros((0, 8), device="cuda"), 2)
     assert got.shape == (0, 2) and w.shape == (0, 2)

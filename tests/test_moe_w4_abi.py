@@ -170,6 +170,7 @@ def test_w4_refusals(call):
     assert call(M=-1) == te.TE_ERR_SHAPE
     assert call(N=-1) == te.TE_ERR_SHAPE
     assert call(N=1 << 30) == te.TE_ERR_SHAPE
+    assert call(N=(1 << 26) + 16) == te.TE_ERR_SHAPE
     assert call(K=(1 << 23) + 32) == te.TE_ERR_SHAPE
     assert call(group=0) == te.TE_ERR_SHAPE
     assert call(group=16) == te.TE_ERR_SHAPE
