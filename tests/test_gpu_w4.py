@@ -94,6 +94,18 @@ def test_w4_gemm(m, n, k, group, dtype):
             check(f64(d), x, w.rows(0, n), None if bias is None else f64(bias), k, group, out)
 
 
+@pytest.mark.parametrize("m", [1, 3, 16, 40])
+@pytest.mark.parametrize("fmt", ["int4", "e2m1"])
+def test_w4_gemm_of_subnormal_activations(m, fmt):
+    """fp16 below 2^-14: whole multiples of 2^-24, none of them lost."""
+    w = Weights(17, 50, 416, 32, fmt, "fp32")
+    rng = np.random.default_rng([403, m])
+    x = torch.from_numpy((rng.integers(-1023, 1024, (m, 416)) * 2.0 ** -24).astype(np.float16)).cuda()
+    assert np.abs(f64(x)).max() < 2.0 ** -14
+    d = te().w4_gemm(x, w.w, fmt, w.s, out_dtype=torch.float32)
+    check(f64(d), x, w.rows(0, 50), None, 416, 32, "fp32")
+
+
 @pytest.mark.parametrize("m,n,k,group", SHAPES)
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_w4_gated_gemm(m, n, k, group, act):
