@@ -593,6 +593,14 @@ te_status w4_by_group(const W4Params& p, hipStream_t stream) {
 //   16 rows: N = 14336 gated, K = 4096 4 waves and 2 slots 21.4, 8 and 3 32.1;  N = K = 4096 (256) 8.2 and 7.9
 //   32 rows: the same N 3 waves 32.0, 7 waves 38.0;  N = 4096, K = 14336 27.9 and 19.5;  64 rows of N = K = 4096 (512 tiles
 //           with their two tiles of rows) 13.6 and 17.0
+// The chunk of K that x and the scales are copied for: 64 steps where 32 are not all of it, if the joints, where every
+// load ends, cost more than the later start.  With 64 and 32 (many tiles: 4 and 2 waves), weights from HBM:
+//   1 row, many tiles: N = 28672 gated, K = 8192 58.3 (4.2 TB/s) and 70.5;  N = 16384, K = 16384, E2M1 in groups of 32
+//           34.8 and 42.4;  N = 16384, K = 6144 16.0 and 17.6, but K = 4608 14.1 and 13.9, K = 5120 in groups of 32 23.0
+//           and 20.7;  N = 14336 gated, K = 4096 21.2 and 17.5
+//   1 row, few: N = 4096, K = 14336 11.7 and 13.1, K = 4608 6.4 and 6.9, but K = 4096 5.6 and 5.1
+//   3 and 4 rows, few: N = 4096, K = 14336 13.7 and 14.7, N = K = 8192 13.3 and 13.5;  many: N = 28672 gated, K = 8192
+//           66.8 and 61.9
 // Two fragments a wave where many tiles are left of them (64 rows over 32 experts, N = 1536: 28.0, one fragment
 // 28.4).
 template <class T, te_w4_format FMT, int NF>
@@ -602,12 +610,14 @@ te_status w4_by_rows(const W4Params& p, int64_t rows, int64_t tiles, hipStream_t
   // a workgroup of the ring kernels has a CU's LDS for itself, or shares it: with tiles of rows beside each other
   const bool ring_many = 2 * tiles * (p.m_splits != nullptr ? 1 : (p.M + 31) / 32) > 3 * cus;
   if (rows <= 1) {
+    if (many && p.K >= 6144) return w4_by_group<T, FMT, W4Few<4, NF, 1, 4, 64>>(p, stream);
     if (many) return w4_by_group<T, FMT, W4Few<2, NF, 1, 2>>(p, stream);
+    if (p.K > 4096) return w4_by_group<T, FMT, W4Few<8, NF, 1, 2, 64>>(p, stream);
     return w4_by_group<T, FMT, W4Few<8, NF, 1, 2>>(p, stream);
   }
   if (rows <= 4) {
     if (many && p.K <= 2048) return w4_by_group<T, FMT, W4Few<2, NF, 4, 2, 16>>(p, stream);
-    if (!many && p.K >= 8192) return w4_by_group<T, FMT, W4Few<8, NF, 4, 2>>(p, stream);
+    if (!many && p.K >= 8192) return w4_by_group<T, FMT, W4Few<8, NF, 4, 2, 64>>(p, stream);
     return w4_by_group<T, FMT, W4Few<4, NF, 4, 2>>(p, stream);
   }
   if (rows <= 16) {

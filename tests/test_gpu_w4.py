@@ -94,6 +94,20 @@ def test_w4_gemm(m, n, k, group, dtype):
             check(f64(d), x, w.rows(0, n), None if bias is None else f64(bias), k, group, out)
 
 
+@pytest.mark.parametrize("m", [1, 4])
+@pytest.mark.parametrize("n,k,group", [(40, 12448, 32), (33, 10240, 128), (17, 8352, 96), (12304, 8352, 32),
+                                       (24592, 8320, 64)])
+def test_w4_gemm_of_a_long_k(m, n, k, group):
+    """K of several chunks, with few and many tiles; the first and the last columns."""
+    for i, (fmt, scales, zeros) in enumerate([("int4", "bf16", True), ("e2m1", "e8m0", False)]):
+        w = Weights(20 + i, n, k, group, fmt, scales, zeros)
+        x = activations(m, m, k, "bf16")
+        d = te().w4_gemm(x, w.w, fmt, w.s, w.zero, out_dtype=torch.float32)
+        for a, b in ((0, 24), (n - 17, n)):
+            b = min(b, n)
+            check(f64(d[:, a:b]), x, w.rows(a, b), None, k, group, "fp32")
+
+
 @pytest.mark.parametrize("m", [1, 3, 16, 40])
 @pytest.mark.parametrize("fmt", ["int4", "e2m1"])
 def test_w4_gemm_of_subnormal_activations(m, fmt):
