@@ -579,7 +579,8 @@ te_status te_mxfp8_grouped_dgated_gemm(int32_t num_groups, const int32_t* m_spli
  *          order of e; -1 where no unmasked expert is left.  Sums with a bias
  *          are compared in 64 bits.
  *   weights[t, k] = scale * s_{experts[t, k]}, divided with normalize = 1 by
- *          the sum of the token's chosen s; 0 where experts[t, k] is -1
+ *          the sum of the token's chosen s (also of scores that fp32 does not
+ *          hold, such as sigmoids of -200); 0 where experts[t, k] is -1
  *   logits   dtype [tokens, num_experts]: TE_BF16, TE_FP16 or TE_FP32;
  *            16-byte aligned
  *   bias     float [num_experts], or NULL: enters the choice alone (load

@@ -4,10 +4,11 @@
 // sigmoid(l_e), the chosen experts e_0, e_1, .. are the topk largest of s_e + bias_e (of l_e without a bias: the
 // scores rise with the logits) in falling order, equal ones in rising order of e, and
 //   w_k = scale s_{e_k} / S,   S = sum over the chosen of s, or 1 (normalize = 0).
-// Backward, with g_k = scale dw_k:
-//   ds_k = (g_k - sum_j g_j w_j / scale) / S   (normalize = 0: ds_k = g_k)
-//   sigmoid:  dl_e = ds_e s_e (1 - s_e)
-//   softmax:  dl_e = s_e (ds_e - sum_j ds_j s_j)   (normalize: the sum is 0, only the chosen have a gradient)
+// Backward, with g_k = scale dw_k and v_k = w_k / scale:
+//   normalize:  d_k = v_k (g_k - sum_j g_j v_j);   softmax: dl = d of the chosen;  sigmoid: dl = d (1 - s) of the chosen
+//   normalize = 0:  sigmoid: dl_e = g_e s_e (1 - s_e);  softmax: dl_e = s_e (g_e - sum_j g_j s_j)
+// Shares do not change if all scores are divided by e^c: softmax takes c so that the largest is 1, sigmoid the largest
+// chosen logit where that is below 0, so that scores that no float holds (logits below -104) have their shares.
 //
 // A token's experts lie in the registers of 16 lanes (more than 256 experts or 16 slots: 64); a slot is a maximum
 // over them.  The forward is bound by its instructions: 16384 tokens of 256 experts, 8 chosen, take 11 us with a bias
@@ -47,8 +48,11 @@ __device__ __forceinline__ float load_logit<float>(const void* p, int64_t i) { r
 
 constexpr float kInf = __builtin_huge_valf();
 
-// 1 / (1 + e^-x) and its derivative, without cancellation on either side.
-__device__ __forceinline__ float sigmoid_of(float x) { return 1.0f / (1.0f + expf(-x)); }
+// e^-c / (1 + e^-x), c <= 0 and c >= x where it is not 0: in range for every x.
+__device__ __forceinline__ float sigmoid_of(float x, float c) {
+  return (x < 0.f ? expf(x - c) : 1.0f) / (1.0f + expf(-fabsf(x)));
+}
+// The derivative of 1 / (1 + e^-x), without cancellation on either side.
 __device__ __forceinline__ float sigmoid_slope(float x) {
   const float e = expf(-fabsf(x));
   return e / ((1.0f + e) * (1.0f + e));
@@ -225,16 +229,12 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteParams p) {
   }
 
   const float mine_l = mine >= 0 ? load_logit<T>(p.logits, at + mine) : -kInf;
-  float w;
-  if (p.sigmoid) {
-    w = mine >= 0 ? sigmoid_of(mine_l) : 0.f;
-  } else {
-    if (p.normalize) {
-      const float m = lanes_all<LANES>(mine_l, most);
-      top = m > -kInf ? m : 0.f;
-    }
-    w = mine >= 0 ? expf(mine_l - top) : 0.f;
+  if (p.normalize) {
+    const float m = lanes_all<LANES>(mine_l, most);
+    top = m > -kInf ? m : 0.f;
   }
+  float w = 0.f;
+  if (mine >= 0) w = p.sigmoid ? sigmoid_of(mine_l, p.normalize ? fminf(top, 0.f) : 0.f) : expf(mine_l - top);
   if (p.normalize) total = lanes_all<LANES>(w, sum);
   if (p.normalize || !p.sigmoid) w = w == 0.f && total == 0.f ? 0.f : w / total;
   if (ok && slot < p.topk) {
@@ -286,23 +286,24 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RoutePara
     }
     total = lanes_all<LANES>(s, sum);
     total = total == 0.f ? 1.f : total;
-  } else if (!p.sigmoid) {
+  } else if (p.normalize) {
     const float m = lanes_all<LANES>(l, most);
     top = m > -kInf ? m : 0.f;
   }
-  // the slot's score (of shares among the chosen: up to the factor that cancels)
-  const float s = e < 0 ? 0.f : p.sigmoid ? sigmoid_of(l) : expf(l - top) / total;
   float c = 0.f;  // what every expert subtracts
   if (p.normalize) {
-    float S = lanes_all<LANES>(s, sum);
-    S = S == 0.f ? 1.f : S;
-    const float gw = lanes_all<LANES>(g * s, sum) / S;
-    g = e < 0 ? 0.f : (g - gw) / S;
-    if (!p.sigmoid) g *= s;
-  } else if (!p.sigmoid) {
-    c = lanes_all<LANES>(g * s, sum);
+    // the slot's score, up to the factor that cancels, and its share
+    float s = e < 0 ? 0.f : p.sigmoid ? sigmoid_of(l, fminf(top, 0.f)) : expf(l - top);
+    const float S = lanes_all<LANES>(s, sum);
+    s = S == 0.f ? 0.f : s / S;
+    const float gw = lanes_all<LANES>(g * s, sum);
+    g = e < 0 ? 0.f : (g - gw) * s;
+    if (p.sigmoid && e >= 0) g *= sigmoid_of(-l, 0.f);
+  } else if (p.sigmoid) {
+    if (e >= 0) g *= sigmoid_slope(l);
+  } else {
+    c = lanes_all<LANES>(e < 0 ? 0.f : g * (expf(l - top) / total), sum);
   }
-  if (p.sigmoid && e >= 0) g *= sigmoid_slope(l);
   __syncthreads();
   if (e >= 0) atomicAdd(&slots[group][e], g);
   __syncthreads();

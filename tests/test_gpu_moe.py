@@ -69,6 +69,62 @@ def test_route(tokens, experts, topk, score):
         assert (np.abs(f64(w) - ww) <= weight_tolerance(f64(x), want, ww) + 1e-40).all(), (dtype, bias, normalize)
 
 
+def low_logits(seed, experts, dtype):
+    """Tokens whose logits lie far below 0, close together: sigmoids around and below the smallest float."""
+    rng = np.random.default_rng([312, seed])
+    base = np.array([-20.0, -80.0, -86.5, -88.5, -92.0, -104.0, -200.0, -10000.0, -65504.0, 0.5])
+    x = base[:, None] + np.where(base[:, None] > -1000, rng.standard_normal((base.size, experts)) * 2, 0)
+    return cuda(x, DTYPES[dtype])
+
+
+def log_shares(x, experts):
+    """(shares, 1 - s) of the chosen experts' sigmoids: log s = -log(1 + e^-l), and the softmax of these."""
+    there = experts >= 0
+    l = np.take_along_axis(x, np.where(there, experts, 0), 1)
+    logs = np.where(there, -np.logaddexp(0, -l), -np.inf)
+    e = np.exp(logs - logs.max(axis=1, keepdims=True))
+    return e / e.sum(axis=1, keepdims=True), np.exp(-np.logaddexp(0, l))
+
+
+@pytest.mark.parametrize("experts,topk", [(3, 2), (40, 8), (256, 16), (300, 20)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_route_shares_of_sigmoids_below_fp32(experts, topk, dtype):
+    """Shares of scores add up to the scale however small the scores are, and their gradient is the formula's.  A share: an
+    exponent rounded to |l - top| 2^-24, two exponentials to 2 units in the last place, 1 + e, quotient (8 + 2 roundings of
+    2^-24 and the argument's), the same of their sum with 6 additions across the lanes, the quotient and the scale."""
+    x = low_logits(experts, experts, dtype)
+    xs = f64(x)
+    got, w = te().moe_route("sigmoid", x, topk, None, True, 2.5)
+    want, _ = oracle.route(xs, topk, "softmax")                        # the scores rise with the logits
+    assert np.array_equal(host(got), want)
+    share, rest = log_shares(xs, want)
+    top = np.take_along_axis(xs, want, 1)
+    r = (2 * (top.max(1) - top.min(1)) + 2 * 12 + 8)[:, None] * U
+    assert (np.abs(f64(w) - 2.5 * share) <= r * 2.5 * share).all()
+    np.testing.assert_allclose(f64(w).sum(axis=1), 2.5, rtol=1e-5)
+    dw = np.random.default_rng([313, experts]).standard_normal((xs.shape[0], topk)).astype(np.float32)
+    g = 2.5 * dw.astype(np.float64)
+    mean = (g * share).sum(axis=1, keepdims=True)
+    grad, big = np.zeros_like(xs), np.zeros_like(xs)
+    np.put_along_axis(grad, want, share * rest * (g - mean), 1)
+    # the share's error, that of the mean (|g| times the shares') with topk additions, 1 - s to 8 roundings
+    np.put_along_axis(big, want, share * rest * (np.abs(g) + (np.abs(g) * share).sum(axis=1, keepdims=True)), 1)
+    d = f64(te().moe_route_backward("sigmoid", x, got, cuda(dw), True, 2.5))
+    tol = REL[dtype] * np.abs(grad) + ABS[dtype] + (2 * r + (topk + 10) * U) * big
+    assert (np.abs(d - grad) <= tol).all(), np.max(np.abs(d - grad) - tol)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_route_sigmoids_among_the_subnormals(dtype):
+    """Scores below 2^-126 are whole multiples of 2^-149: off by 3 steps of the exponential, the quotient and the scale,
+    beside their relative error (the exponent's argument is the logit itself; 8 roundings)."""
+    x = low_logits(7, 64, dtype)
+    got, w = te().moe_route("sigmoid", x, 8, None, False, 1.0)
+    l = np.take_along_axis(f64(x), host(got).astype(np.int64), 1)
+    s = np.exp(-np.logaddexp(0, -l))
+    assert (np.abs(f64(w) - s) <= 10 * U * s + 4 * 2.0 ** -149).all()
+
+
 @pytest.mark.parametrize("experts,topk", [(16, 16), (200, 9), (1024, 64)])
 def test_route_equal_logits_go_to_the_lowest_expert(experts, topk):
     for value in (0.0, -3.0, 7.5):
