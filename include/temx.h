@@ -702,6 +702,10 @@ te_status te_moe_combine_backward(const void* dy, const void* rows, te_dtype dty
  *   M == 0 or N == 0 enqueues nothing; K == 0 gives P = bias.
  *   x, w and d are 16-byte aligned; scales and bias to their type.  d may not
  *   overlap an input.
+ *   Rounding errors are relative to the sums of |x| |w_scale| |q|, with TE_W4_INT4
+ *   of |x| |w_scale| (q + z): the zero point's part is a sum of its own.  A finite
+ *   x gives what P gives wherever P itself is in fp32's range.  With bf16 x sums
+ *   are held in steps of 2^-134, with fp16 x of 2^-149 (before w_scale).
  *   A non-finite value of x affects its own row of D only; with TE_W4_INT4 an
  *   infinite one gives NaN where the formula gives an infinity.
  */

@@ -68,23 +68,29 @@ constexpr int kStep = 128;              // K of a wave's step: 4 blocks of 32
 constexpr int kBeyond = 0x60000000;     // an offset past the end of every buffer below (2^30 bytes at most): zeros
 
 template <class T> struct Half;  // the activations' type in the MFMA
+// Weights enter in units of 1 / kUnit, and the sums are multiplied by it once, at the end: 128 products of a bf16 value
+// and a code or zero point (up to 255 < 2^15 / 128) then stay in range where the values themselves do, and a group's
+// sum before its scale and before its zero point's part is taken off cannot overflow.  The price are the last 15 of the
+// 149 binary places below 1, sums below 2^-111 that lose some of theirs.  fp16 values are at most 2^16.
 template <> struct Half<bf16_t> {
   typedef v8bf v8;
+  static constexpr float kUnit = 32768.f;
   static __device__ __forceinline__ v4f mfma(v8 a, v8 b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
   template <bool HI>
   static __device__ __forceinline__ uint32_t from_e4m3(uint32_t v) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 512.f, HI));
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 512.f / kUnit, HI));
   }
   template <int BYTE>
   static __device__ __forceinline__ uint32_t from_e2m1(uint32_t v) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, 1.f, BYTE));
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, 1.f / kUnit, BYTE));
   }
-  static constexpr uint32_t ones = 0x3F803F80u;
+  static constexpr uint32_t ones = 0x38003800u;  // 1 / kUnit
 };
 template <> struct Half<f16_t> {
   typedef v8h v8;
+  static constexpr float kUnit = 1.f;
   static __device__ __forceinline__ v4f mfma(v8 a, v8 b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
   }
@@ -362,6 +368,8 @@ struct W4Sums {
         v += part[(w * NF * MF + f * MF + (m >> 4)) * 256 + at];
         if (job.gated) up += part[(w * NF * MF + (NF - 1) * MF + (m >> 4)) * 256 + at];
       }
+      v *= Half<T>::kUnit;
+      up *= Half<T>::kUnit;
       if (p.bias != nullptr) {
         v += to_float(static_cast<const T*>(p.bias)[job.w_row + n]);
         if (job.gated) up += to_float(static_cast<const T*>(p.bias)[job.w_row + p.N + n]);

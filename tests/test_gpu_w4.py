@@ -120,6 +120,47 @@ def test_w4_gemm_of_subnormal_activations(m, fmt):
     check(f64(d), x, w.rows(0, 50), None, 416, 32, "fp32")
 
 
+@pytest.mark.parametrize("m", [1, 3, 16, 40])
+@pytest.mark.parametrize("fmt,scales,zeros", [("int4", "bf16", False), ("int4", "fp32", True), ("int4", "e8m0", 255),
+                                              ("e2m1", "e8m0", False)])
+@pytest.mark.parametrize("k,group", [(416, 32), (1024, 128), (576, 96)])
+def test_w4_gemm_of_the_largest_activations(m, fmt, scales, zeros, k, group):
+    """bf16 up to its largest value, where sum x q and z sum x pass fp32's range and the results do not."""
+    w = Weights(18, 50, k, group, fmt, scales, bool(zeros))
+    if zeros == 255:
+        w.z[:] = 255
+        w.zero = torch.from_numpy(w.z).cuda()
+    if scales != "e8m0":                                               # 0.002 .. 0.02 over 32, so that sums stay in range
+        w.s = w.s / 32
+        w.values = f64(w.s)
+    else:
+        w.s = w.s - 20
+        w.values = 2.0 ** (w.s.cpu().numpy().astype(np.float64) - 127)
+    rng = np.random.default_rng([404, m])
+    x = rng.choice([-1.0, 1.0], (m, k)) * rng.uniform(0.5, 1.0, (m, k)) * 3.3e38
+    x = torch.from_numpy(x.astype(np.float32)).cuda().bfloat16()
+    d = te().w4_gemm(x, w.w, fmt, w.s, w.zero, out_dtype=torch.float32)
+    assert torch.isfinite(d).all()
+    check(f64(d), x, w.rows(0, 50), None, k, group, "fp32")
+
+
+@pytest.mark.parametrize("m", [1, 3, 16, 40])
+@pytest.mark.parametrize("fmt,zeros", [("int4", False), ("int4", True), ("e2m1", False)])
+def test_w4_gemm_of_the_smallest_activations(m, fmt, zeros):
+    """bf16 around 2^-118: sums are held in steps of 2^-134 (scales of 1), off by half of one for each addition of a chain
+    and each group beside their relative error."""
+    w = Weights(19, 50, 416, 32, fmt, "fp32", zeros)
+    w.s = torch.ones_like(w.s)
+    w.values = f64(w.s)
+    rng = np.random.default_rng([405, m])
+    x = torch.from_numpy((rng.standard_normal((m, 416)) * 2.0 ** -118).astype(np.float32)).cuda().bfloat16()
+    d = te().w4_gemm(x, w.w, fmt, w.s, w.zero, out_dtype=torch.float32)
+    p, s = oracle.w4_gemm(f64(x), *w.rows(0, 50), None)
+    steps = 416 / 8 + 2 * 416 / 32 + 16
+    most = 1 + (15 if zeros else 8 if fmt == "int4" else 0)            # the zero point multiplies its sum's error
+    assert (np.abs(f64(d) - p) <= tolerance(p, s, 416, 32, "fp32") + steps * most * 2.0 ** -135).all()
+
+
 @pytest.mark.parametrize("m,n,k,group", SHAPES)
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_w4_gated_gemm(m, n, k, group, act):
