@@ -622,7 +622,8 @@ te_status te_moe_route_backward(te_score score, const void* logits, te_dtype dty
  *   slots 0 .. 2^31 - 65536, num_experts 1 .. 1024; all pointers 4-byte aligned
  *   workspace device scratch of at least te_moe_sort_workspace_size(slots,
  *             num_experts) bytes, 4-byte aligned (NULL where that is 0).  Calls
- *             that may run at the same time need workspaces of their own.
+ *             that may run at the same time need workspaces of their own.  The
+ *             size never falls as slots or num_experts grow.
  *   No output and no workspace may overlap an input or another output.
  * slots == 0 writes zeros to m_splits.
  */

@@ -578,7 +578,8 @@ extern "C" te_status te_moe_route_backward(te_score score, const void* logits, t
 
 extern "C" size_t te_moe_sort_workspace_size(int64_t slots, int32_t num_experts) {
   if (slots <= 0 || slots > kMostSlots || num_experts < 1 || num_experts > kMaxExperts) return 0;
-  const int64_t blocks = sort_blocks(slots);
+  // that of runs of kSortRun, which are more than the longer ones: a batch's workspace serves every smaller one
+  const int64_t blocks = std::min<int64_t>((slots + kSortRun - 1) / kSortRun, kSortBlocks);
   return blocks == 1 ? 0 : (size_t)(blocks * num_experts) * sizeof(int32_t);
 }
 

@@ -84,6 +84,17 @@ def test_sort_workspace_size():
         assert most <= 4 * 256 * n
 
 
+def test_sort_workspace_of_the_largest_batch_serves_every_smaller_one():
+    size = te.te_moe_sort_workspace_size
+    slots = sorted({s + d for s in (2048, 4096, 1 << 17, 1 << 19, 1 << 20, 3 << 19, 1 << 24, MOST - 1) for d in (-1, 0, 1)}
+                   | set(range(1 << 18, 1 << 21, 30011)))
+    for n in (1, 60, 1024):
+        sizes = [size(s, n) for s in slots]
+        assert sizes == sorted(sizes)
+    for s in (100, 5000, 1 << 19, (1 << 19) + 1, MOST):
+        assert [size(s, n) for n in (1, 8, 1024)] == sorted(size(s, n) for n in (1, 8, 1024))
+
+
 def dispatch(x=P, dt=te.TE_BF16, tokens=4, cols=64, row=P2, topk=2, rows=8, y=P3, q=None, qs=None, qf=te.TE_E4M3):
     return L.te_moe_dispatch(x, dt, tokens, cols, row, topk, rows, y, q, qs, qf, None)
 
