@@ -590,7 +590,9 @@ te_status te_mxfp8_grouped_dgated_gemm(int32_t num_groups, const int32_t* m_spli
  *   num_experts 1 .. 1024, topk 1 .. min(num_experts, 64), tokens >= 0,
  *   tokens * topk < 2^31 - 65536.  No output may overlap an input.
  * An expert whose logit (or logit's sum with the bias) is NaN is not chosen; a
- * NaN logit makes the softmax shares (normalize = 0) of its token NaN.
+ * NaN logit makes the softmax shares (normalize = 0) of its token NaN, as one of
+ * +inf makes all its softmax weights, and with a bias either makes all its sums
+ * NaN: none is chosen.
  */
 te_status te_moe_route(te_score score, const void* logits, te_dtype dtype, int64_t tokens, int32_t num_experts,
                        int32_t topk, const float* bias, int normalize, float scale, int32_t* experts, float* weights,

@@ -236,7 +236,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteParams p) {
   float w = 0.f;
   if (mine >= 0) w = p.sigmoid ? sigmoid_of(mine_l, p.normalize ? fminf(top, 0.f) : 0.f) : expf(mine_l - top);
   if (p.normalize) total = lanes_all<LANES>(w, sum);
-  if (p.normalize || !p.sigmoid) w = w == 0.f && total == 0.f ? 0.f : w / total;
+  if (mine >= 0 && (p.normalize || !p.sigmoid)) w /= total;  // the total of a token with a NaN logit may be NaN
   if (ok && slot < p.topk) {
     p.experts[token * p.topk + slot] = mine;
     p.weights[token * p.topk + slot] = p.scale * w;

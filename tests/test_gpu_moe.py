@@ -183,6 +183,27 @@ def test_route_masked_infinite_and_nan():
     np.testing.assert_allclose(f64(w)[0], [0.25] * 4 + [0.0] * 5, rtol=1e-6)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("normalize", [True, False])
+@pytest.mark.parametrize("experts", [9, 300])
+def test_route_slots_without_an_expert_weigh_nothing(score, normalize, experts):
+    """Whatever the token's other logits are: NaN and infinite ones make the softmax NaN, but not its empty slots; with a
+    bias, every sum of such a token is NaN and none of its experts is chosen."""
+    x = np.full((4, experts), -np.inf, dtype=np.float32)
+    x[:, 2], x[0, 5], x[1, 5], x[2, 5] = 1.0, np.nan, np.inf, -np.inf
+    for dtype in ("fp32", "bf16"):
+        for bias in (None, torch.zeros(experts, device="cuda")):
+            e, w = te().moe_route(score, cuda(x, DTYPES[dtype]), 4, bias, normalize)
+            e, w = host(e), f64(w)
+            want = [[2], [5, 2], [2], [2]]
+            if bias is not None and score == "softmax":
+                want[:2] = [], []
+            for t in range(4):
+                assert e[t].tolist() == want[t] + [-1] * (4 - len(want[t]))
+            assert (w[e < 0] == 0).all()
+            assert np.isfinite(w[2:]).all() and (w[2:, 0] > 0).all()
+
+
 def test_route_of_more_tokens_than_a_launch_takes():
     """Two launches: tokens on both sides of the border and the last ones, against the same tokens alone."""
     tokens = (1 << 25) + 1001
