@@ -427,6 +427,28 @@ def test_combine_backward_to_mxfp8_is_the_quantized_gradient(tokens, topk, cols,
     assert torch.equal(dw2, dw)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_mxfp8_rows_of_special_values(fmt):
+    """Blocks of NaN, infinities, both zeros, subnormals and the largest values: as the quantize kernel takes them."""
+    x = values(10, (12, 96), "bf16")
+    inf, nan, big, low = float("inf"), float("nan"), 3.3895e38, 2.0 ** -133
+    for t, v in enumerate((nan, inf, -inf, 0.0, -0.0, low, -low, big, -big, 2.0 ** -126)):
+        x[t, 32:64] = v
+        x[t, 70] = v
+    x[10], x[11, 1::2] = low, -0.0
+    row, slot = slots_of(12, 12, 5, 3, False)
+    ones = torch.ones((12, 3), device="cuda")
+    _, q, s = te().moe_dispatch(x, cuda(row), fmt, want_y=False)
+    drows, _, q2, s2 = te().moe_combine_backward(x, values(11, (36, 96), "bf16"), cuda(row), ones, fmt)
+    qx, sx, _, _ = te().mxfp8_quantize(x, fmt, "row")
+    token = slot // 3
+    assert np.array_equal(host(q), host(qx)[token]) and np.array_equal(host(s), host(sx)[token])
+    qd, sd, _, _ = te().mxfp8_quantize(drows, fmt, "row")
+    assert np.array_equal(host(q2), host(qd)) and np.array_equal(host(s2), host(sd))
+    same = ~np.isnan(f64(x))[token]
+    assert np.array_equal(f64(drows)[same], f64(x)[token][same]) and np.isnan(f64(drows)[~same]).all()
+
+
 def test_rows_outside_are_not_touched():
     """Bad row numbers are left out: nothing is read or written outside the tensors."""
     big = torch.full((40, 64), 7.0, dtype=torch.bfloat16, device="cuda")
