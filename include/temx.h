@@ -700,8 +700,9 @@ te_status te_moe_combine_backward(const void* dy, const void* rows, te_dtype dty
  *   w_zero   uint8 [N, K/group_size], or NULL
  *   d        [M, N], d_dtype dtype or TE_FP32
  *   bias     dtype [N], or NULL
- *   Shapes: any M, N >= 0 (any M is right; from about 64 rows up a GEMM on
- *   quantized activations is the faster one); M < 2^31 - 65536, N <= 2^26, K <= 2^23.
+ *   Shapes: any M, N >= 0 (any M is right, but the weights are read once for
+ *   each 32 rows: from about 64 rows up an MXFP8 GEMM is the faster one where
+ *   the weights are there in that format too); M < 2^31 - 65536, N <= 2^26, K <= 2^23.
  *   M == 0 or N == 0 enqueues nothing; K == 0 gives P = bias.
  *   x, w and d are 16-byte aligned; scales and bias to their type.  d may not
  *   overlap an input.

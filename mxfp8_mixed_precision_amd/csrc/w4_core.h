@@ -17,10 +17,10 @@
 // the more rows: a CU takes in ~75 bytes a ns from L2, 917 KB of 32 x 14336 in 12 us.  Loading x and the scales where
 // they are used, straight into the MFMA's layout, took 1.5 to 2 times as long: such a load takes 64 bytes of each of 16
 // rows, and loads return in order, so that each waits for the weights' ones before it.
-// Measured on MI355X, us a kernel, inputs of three calls in turn: one row, N = 14336 gated, K = 4096, groups of 128:
-// 15.6 (61 MB, 3.9 TB/s; with its caller's other calls around it 14.0, 4.3 TB/s; a large copy 5.0); 64 rows over 32
-// experts, N = 1536, K = 4096: 27 (91 MB); 32 rows, N = 4096, K = 14336, E2M1 in groups of 32: 18.3 (39 MB of weights
-// and x); 5 rows, N = 1001, K = 2080: 6.2, latencies.
+// Measured on MI355X, us a kernel, weights from HBM (calls in turn of more than 700 MB, from a graph) and of three calls
+// in turn, which the last-level cache holds: one row, N = 14336 gated, K = 4096, groups of 128: 16.1 and 15.6 (61 MB, 3.8
+// TB/s; a large copy 5.0); 64 rows over 32 experts, N = 1536, K = 4096: 27.3 and 26.8 (91 MB); 32 rows, N = 4096, K =
+// 14336, E2M1 in groups of 32: 23.2 and 18.5 (39 MB of weights and x); 5 rows, N = 1001, K = 2080: 6.1, latencies.
 #pragma once
 
 #include "gemm_core.h"
@@ -642,7 +642,11 @@ te_status w4_run(W4Params p, hipStream_t stream) {
   p.blocks_of_group = p.group / 32;
   p.group_magic = (((uint64_t)1 << 40) + p.blocks_of_group - 1) / p.blocks_of_group;
   const bool grouped = p.m_splits != nullptr;
-  // rows of a tile: all, or those of an expert on average and one more
+  // Rows of a tile: all, or those of an expert on average and one more, since the host does not know the splits.  An
+  // expert with more is walked in several tiles, and the launch waits for it.  us of an even batch, with a quarter and
+  // with half of its rows on one expert, by this rule (tiles of 1 or 4 rows) and in tiles of 16: 64 rows over 64 experts,
+  // N = 1536, K = 4096 34.7, 34.9, 51.7 and 44.3, 40.5, 33.9;  N = 512 gated, K = 1024 11.0, 19.6, 32.3 and 15.5, 14.7,
+  // 12.7;  64 over 32, N = 1536, K = 4096 28.5, 34.1, 52.1 and 31.0, 30.5, 29.1
   const int64_t rows = grouped ? p.M / p.groups + 1 : p.M, experts = grouped ? std::min<int64_t>(p.groups, p.M) : 1;
   const int64_t tiles = (p.N + 15) / 16 * experts;
   if (p.act >= 0) return w4_by_rows<T, FMT, 2>(p, rows, tiles, stream);

@@ -45,7 +45,7 @@ def shares(s, experts, normalize=True) -> np.ndarray:
     live = experts >= 0
     w = np.where(live, np.take_along_axis(s, np.where(live, experts, 0), 1), 0.0)
     if normalize:
-        # in the log domain's stead: scores too small for float64 do not occur in the tests
+        # in the log domain's stead: tests of scores too small for float64 have their logarithms
         total = w.sum(axis=1, keepdims=True)
         w = w / np.where(total == 0, 1.0, total)
     return w
