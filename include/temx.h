@@ -708,8 +708,9 @@ te_status te_moe_combine_backward(const void* dy, const void* rows, te_dtype dty
  *   overlap an input.
  *   Rounding errors are relative to the sums of |x| |w_scale| |q|, with TE_W4_INT4
  *   of |x| |w_scale| (q + z): the zero point's part is a sum of its own.  A finite
- *   x gives what P gives wherever P itself is in fp32's range.  With bf16 x sums
- *   are held in steps of 2^-134, with fp16 x of 2^-149 (before w_scale).
+ *   x gives what P gives wherever P itself is in fp32's range.  Groups' sums
+ *   before w_scale, and their total after it, are held in steps of 2^-134 with
+ *   bf16 x, of 2^-149 with fp16 x.
  *   A non-finite value of x affects its own row of D only; with TE_W4_INT4 an
  *   infinite one gives NaN where the formula gives an infinity.
  */
